@@ -104,6 +104,31 @@ __device__ __forceinline__ size_t cache_row_read(const headq_cache& c, int b, in
   return static_cast<size_t>(s.slab) * slab_rows(c) + s.off;
 }
 
+// A sequence's tokens in a packed batch (headq_span): its first row, how many rows
+// (0 <= n <= span.n, all inside the packed tensors), its cached tokens and the position
+// of its first row's token; p0 < 0 when it has more rows than cached tokens and so
+// takes no part.
+struct SpanSeq {
+  int row0, n, T, p0;
+};
+
+__device__ __forceinline__ SpanSeq span_seq(const headq_span& s, int b) {
+  SpanSeq q;
+  q.T = s.seq_lens ? max(0, min(s.seq_lens[b], s.T)) : s.T;
+  if (s.cu) {
+    const int r0 = s.cu[b], r1 = s.cu[b + 1];
+    const bool ok = r0 >= 0 && r1 >= r0 && r1 <= s.rows;
+    q.row0 = ok ? r0 : 0;
+    q.n = ok ? r1 - r0 : 0;
+  } else {
+    q.row0 = b * s.n;  // B * n <= rows, checked on the host
+    q.n = s.n;
+  }
+  q.p0 = q.T - q.n;
+  q.n = min(q.n, s.n);
+  return q;
+}
+
 struct CacheWriteParams {
   headq_cache c;
   const void* k;
@@ -116,9 +141,43 @@ struct CacheWriteParams {
   bool append;
   const int32_t* seq_lens;
   int T;
+  // packed batch (headq_cache_write_ragged): element strides of k and v, the gather
+  long long k_row, k_head, v_row, v_head;
+  headq_span span;
+  const int32_t* src;
+  int src_rows;
   // 1.0f, set by the host: a value the compiler cannot see, so that the packed
   // "multiply, then add" of the codec is not contracted (codec::fma2)
   float one;
+};
+
+struct CacheReadParams {
+  headq_cache c;
+  headq_span span;
+  const float* U;
+  float sigma;
+  headq_rows k, v;  // outputs; ptr null: not wanted
+  unsigned* err;    // nullable
+};
+
+// headq_tree_attn.  Query row x = i * G + g of a (b, kv) unit: new token i, query head
+// kv * G + g.  Partials of a T-split: o [unit][split][n * G][d] unnormalised, then
+// (running max in natural-log units, sum) [unit][split][n * G].
+struct TreeParams {
+  headq_cache c;
+  headq_rows q, out;
+  int Hq, G;
+  headq_span span;
+  const uint8_t* mask;
+  long long mask_stride;
+  const float* U;
+  float sm_scale;
+  float corr_sign;
+  float* lse;
+  int splits, chunk;
+  float* part_o;
+  float2* part_ml;
+  unsigned* err;
 };
 
 // Decode split partials: unnormalised outputs o [B*Hq][splits][d] (rows of d
@@ -202,6 +261,8 @@ headq_status check_read_args(const headq_cache* c, const void* q, headq_dtype qd
                              const float* U, int corr_sign);
 
 cudaError_t launch_cache_write(const CacheWriteParams& p, cudaStream_t s);
+cudaError_t launch_cache_write_ragged(const CacheWriteParams& p, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheReadParams& p, cudaStream_t s);
 cudaError_t launch_attn_kl(const AttnKlParams& p, cudaStream_t s);
 // the tensor-core diagnostic kernel (attn_kl_hm.cu): its shapes, its split plan
 // and its launch (the split kernel only; the combine kernel follows it)

@@ -1,0 +1,40 @@
+// Shared by the kernels of headq_tree_attn.
+#pragma once
+
+#include "headq_internal.cuh"
+
+namespace headq {
+
+// T-splits per (sequence, KV head) and tokens per split
+struct TreePlan {
+  int splits, chunk;
+};
+TreePlan tree_plan(const headq_cache& c, int Hq, int n, int T, bool q_bf16);
+cudaError_t launch_tree(const TreeParams& p, cudaStream_t s);
+
+// whether new token i of sequence b sees its new token j (both below span.n)
+__device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int i, int j) {
+  return p.mask ? p.mask[b * p.mask_stride + static_cast<long long>(i) * p.span.n + j] != 0 : j <= i;
+}
+
+// 4 channels of a 2-bit code: min + code * scale
+__device__ __forceinline__ float4 decode4(uint32_t byte, float scale, float mn) {
+  return make_float4(fmaf(static_cast<float>(byte & 3u), scale, mn),
+                     fmaf(static_cast<float>((byte >> 2) & 3u), scale, mn),
+                     fmaf(static_cast<float>((byte >> 4) & 3u), scale, mn),
+                     fmaf(static_cast<float>((byte >> 6) & 3u), scale, mn));
+}
+
+// 4 channels of an output row, rounded to its dtype
+__device__ __forceinline__ void store_row4(const headq_rows& o, size_t off, float4 x) {
+  if (o.dtype == HEADQ_BF16) {
+    uint2 u;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(x.y), "f"(x.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(x.w), "f"(x.z));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(o.ptr) + off) = u;
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(o.ptr) + off) = x;
+  }
+}
+
+}  // namespace headq

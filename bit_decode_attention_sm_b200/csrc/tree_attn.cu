@@ -1,0 +1,324 @@
+// headq_tree_attn: several new tokens per sequence attend over the HeadQ cache, the new
+// ones among themselves under a tree mask ("HeadQ: Model-Visible Distortion and
+// Score-Space Correction for KV-Cache Quantization", gist.science summary, section 3,
+// step 3: base logit plus the side code's score-space correction; softmax and readout of
+// section 2.2).  This file: the split plan, the fp32 kernel for every shape, the merge of
+// the splits.  The tensor-core kernel is tree_mma.cu.
+//
+// tree_any_kernel: one CTA per (32 query rows, split, sequence x KV head).  32-token
+// tiles are decoded once into shared memory as rows of d key channels followed by the r
+// side-code entries, the query rows as q followed by U_h^T q, so that one dot product of
+// length d + r is the corrected logit.  Softmax statistics and outputs stay in registers
+// (8 lanes per query row).  Bound by its shared-memory reads (two 16-byte loads per four
+// multiply-adds): it serves fp32 queries and the shapes the tensor-core kernel does not
+// take.
+#include <math.h>
+
+#include "codec.cuh"
+#include "tree.cuh"
+
+namespace headq {
+namespace {
+
+constexpr int kRT = 32;   // query rows per CTA
+constexpr int kTT = 32;   // tokens per tile
+constexpr int kThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// float4 chunks per key / query row in shared memory: odd, so that 8 rows read at the
+// same chunk fall in distinct banks
+__host__ __device__ inline int row_chunks(int d, int r) { return ((d + r + 3) / 4) | 1; }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+tree_any_kernel(const TreeParams p) {
+  constexpr int NC = D / 4 > 8 ? D / 32 : 1;  // value chunks per lane
+  extern __shared__ float4 smem4[];
+  const int r = p.c.r, rc = row_chunks(D, r);
+  float4* q_s = smem4;                     // [kRT][rc]
+  float4* k_s = q_s + kRT * rc;            // [kTT][rc]
+  float4* v_s = k_s + kTT * rc;            // [kTT][D / 4]
+  float* s_s = reinterpret_cast<float*>(v_s + kTT * (D / 4));  // [kRT][kTT + 1]
+  __shared__ long long row_s[kTT];
+
+  const int tid = threadIdx.x;
+  const int unit = blockIdx.z, b = unit / p.c.Hkv, kv = unit - b * p.c.Hkv;
+  const int split = blockIdx.y;
+  const SpanSeq sq = span_seq(p.span, b);
+  const int rows = sq.n * p.G, x0 = blockIdx.x * kRT;
+  if (x0 >= rows) return;
+  const int L = sq.p0 < 0 ? 0 : sq.p0 + sq.n;  // tokens the call reads; none when it takes no part
+  const int t_lo = split * p.chunk, t_hi = min(L, t_lo + p.chunk);
+
+  // query rows, then U_h^T q
+  const bool qb = p.q.dtype == HEADQ_BF16;
+  float* qf = reinterpret_cast<float*>(q_s);
+  for (int e = tid; e < kRT * D; e += kThreads) {
+    const int x = e / D, c = e - x * D, xr = x0 + x;
+    float v = 0.0f;
+    if (xr < rows) {
+      const int i = xr / p.G, g = xr - i * p.G;
+      v = load_elem(p.q.ptr, (sq.row0 + i) * p.q.row_stride + (kv * p.G + g) * p.q.head_stride + c, qb);
+    }
+    qf[x * rc * 4 + c] = v;
+  }
+  __syncthreads();
+  const int r4 = (r + 3) / 4 * 4;
+  for (int e = tid; e < kRT * r4; e += kThreads) {
+    const int x = e / r4, i = e - x * r4;
+    float a = 0.0f;
+    if (i < r) {
+      const float* up = p.U + static_cast<size_t>(kv) * D * r + i;
+      for (int c = 0; c < D; ++c) a = fmaf(qf[x * rc * 4 + c], up[c * r], a);
+    }
+    qf[x * rc * 4 + D + i] = a * p.corr_sign;
+  }
+
+  // this thread's row and channels in the softmax and readout
+  const int orow = tid >> 3, l8 = tid & 7;
+  float m = -INFINITY, l = 0.0f;
+  float4 acc[NC];
+#pragma unroll
+  for (int k = 0; k < NC; ++k) acc[k] = make_float4(0, 0, 0, 0);
+  const int sy = tid >> 4, sx = tid & 15;  // logits of rows sy, sy+16 x tokens sx, sx+16
+  const int len4 = (D + r4) / 4;
+
+  for (int t0 = t_lo; t0 < t_hi; t0 += kTT) {
+    __syncthreads();  // the previous tile (and the query rows) are done with
+    if (tid < kTT) {
+      const int t = t0 + tid;
+      row_s[tid] = t < t_hi ? static_cast<long long>(cache_row_read(p.c, b, kv, t, p.err)) : -1;
+    }
+    __syncthreads();
+    for (int e = tid; e < kTT * (D / 4); e += kThreads) {
+      const int tt = e / (D / 4), c4 = e - tt * (D / 4);
+      const long long row = row_s[tt];
+      float4 k = make_float4(0, 0, 0, 0), v = k;
+      if (row >= 0) {
+        const size_t gr = row * num_groups(D) + 4 * c4 / group_size(D);
+        k = decode4(p.c.k_codes[row * (D / 4) + c4], p.c.k_scale[gr], p.c.k_min[gr]);
+        if (p.c.vmode == HEADQ_V_2BIT) {
+          v = decode4(p.c.v_codes[row * (D / 4) + c4], p.c.v_scale[gr], p.c.v_min[gr]);
+        } else if (p.c.v_dtype == HEADQ_F32) {
+          v = reinterpret_cast<const float4*>(p.c.v)[row * (D / 4) + c4];
+        } else {
+          const uint2 u = reinterpret_cast<const uint2*>(p.c.v)[row * (D / 4) + c4];
+          v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                          __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+        }
+      }
+      k_s[tt * rc + c4] = k;
+      v_s[tt * (D / 4) + c4] = v;
+    }
+    float* kf = reinterpret_cast<float*>(k_s);
+    for (int e = tid; e < kTT * r4; e += kThreads) {
+      const int tt = e / r4, i = e - tt * r4;
+      const long long row = row_s[tt];
+      kf[tt * rc * 4 + D + i] =
+          row >= 0 && i < r ? nibble(p.c.z_codes + row * (r / 2), i) * p.c.z_scale[row] : 0.0f;
+    }
+    __syncthreads();
+
+    float s[2][2] = {{0, 0}, {0, 0}};
+    for (int c = 0; c < len4; ++c) {
+      float4 a[2], w[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) a[k] = q_s[(sy + 16 * k) * rc + c];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) w[k] = k_s[(sx + 16 * k) * rc + c];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          s[i][j] = fmaf(a[i].x, w[j].x, s[i][j]);
+          s[i][j] = fmaf(a[i].y, w[j].y, s[i][j]);
+          s[i][j] = fmaf(a[i].z, w[j].z, s[i][j]);
+          s[i][j] = fmaf(a[i].w, w[j].w, s[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int x = x0 + sy + 16 * i, t = t0 + sx + 16 * j;
+        const bool see = x < rows && t < t_hi && (t < sq.p0 || tree_sees(p, b, x / p.G, t - sq.p0));
+        s_s[(sy + 16 * i) * (kTT + 1) + sx + 16 * j] = see ? s[i][j] * p.sm_scale : -INFINITY;
+      }
+    __syncthreads();
+
+    float* sr = s_s + orow * (kTT + 1);
+    float sv[4], mx = m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      sv[k] = sr[l8 + 8 * k];
+      mx = fmaxf(mx, sv[k]);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    const float f = exp2f((m - base) * kLog2e);  // m = -inf: 0
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float e = exp2f((sv[k] - base) * kLog2e);  // differences are taken before the scaling
+      sum += e;
+      sr[l8 + 8 * k] = e;
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = l * f + sum;
+    m = mx;
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      acc[k].x *= f; acc[k].y *= f; acc[k].z *= f; acc[k].w *= f;
+    }
+    __syncwarp();
+    const int nt = min(kTT, t_hi - t0);
+    for (int tt = 0; tt < nt; ++tt) {
+      const float e = sr[tt];
+      if (e == 0.0f) continue;  // a masked token's values are not looked at
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        if (D / 4 < 8 && l8 >= D / 4) continue;
+        const float4 v = v_s[tt * (D / 4) + l8 + 8 * k];
+        acc[k].x = fmaf(e, v.x, acc[k].x);
+        acc[k].y = fmaf(e, v.y, acc[k].y);
+        acc[k].z = fmaf(e, v.z, acc[k].z);
+        acc[k].w = fmaf(e, v.w, acc[k].w);
+      }
+    }
+  }
+
+  const int x = x0 + orow;
+  if (x >= rows) return;
+  if (p.splits > 1) {
+    const size_t pr = (static_cast<size_t>(unit) * p.splits + split) * (static_cast<size_t>(p.span.n) * p.G) + x;
+#pragma unroll
+    for (int k = 0; k < NC; ++k)
+      if (l8 + 8 * k < D / 4) reinterpret_cast<float4*>(p.part_o + pr * D)[l8 + 8 * k] = acc[k];
+    if (l8 == 0) p.part_ml[pr] = make_float2(m, l);
+    return;
+  }
+  const int i = x / p.G, g = x - i * p.G;
+  const size_t orow_g = static_cast<size_t>(sq.row0) + i;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int k = 0; k < NC; ++k) {
+    const int c4 = l8 + 8 * k;
+    if (c4 >= D / 4) continue;
+    const float4 o = make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
+    store_row4(p.out, orow_g * p.out.row_stride + (kv * p.G + g) * p.out.head_stride + 4 * c4, o);
+  }
+  if (p.lse && l8 == 0) p.lse[orow_g * p.Hq + kv * p.G + g] = l == 0.0f ? -INFINITY : m + logf(l);
+}
+
+// One warp per query row: out = sum_s e^{m_s - M} o_s / sum_s e^{m_s - M} l_s over the
+// splits.  A row that sees nothing (every m_s = -inf) gets 0 and -inf.
+template <int D>
+__global__ void __launch_bounds__(128)
+tree_merge_kernel(const TreeParams p) {
+  const int unit = blockIdx.y, b = unit / p.c.Hkv, kv = unit - b * p.c.Hkv;
+  const SpanSeq sq = span_seq(p.span, b);
+  const int x = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (x >= sq.n * p.G) return;
+  constexpr int NC = (D / 4 + 31) / 32;
+  const size_t ru = static_cast<size_t>(p.span.n) * p.G;
+  const size_t pr = static_cast<size_t>(unit) * p.splits * ru + x;
+  float M = -INFINITY;
+  for (int s = lane; s < p.splits; s += 32) M = fmaxf(M, p.part_ml[pr + s * ru].x);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float base = M == -INFINITY ? 0.0f : M;
+  float L = 0.0f;
+  float4 acc[NC];
+#pragma unroll
+  for (int k = 0; k < NC; ++k) acc[k] = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = p.part_ml[pr + s * ru];
+    const float w = exp2f((ml.x - base) * kLog2e);
+    L = fmaf(w, ml.y, L);
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      if (lane + 32 * k >= D / 4) continue;
+      const float4 o = reinterpret_cast<const float4*>(p.part_o + (pr + s * ru) * D)[lane + 32 * k];
+      if (ml.y != 0.0f) {
+        acc[k].x = fmaf(w, o.x, acc[k].x);
+        acc[k].y = fmaf(w, o.y, acc[k].y);
+        acc[k].z = fmaf(w, o.z, acc[k].z);
+        acc[k].w = fmaf(w, o.w, acc[k].w);
+      }
+    }
+  }
+  const int i = x / p.G, g = x - i * p.G;
+  const size_t orow = static_cast<size_t>(sq.row0) + i;
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+  for (int k = 0; k < NC; ++k) {
+    const int c4 = lane + 32 * k;
+    if (c4 >= D / 4) continue;
+    store_row4(p.out, orow * p.out.row_stride + (kv * p.G + g) * p.out.head_stride + 4 * c4,
+               make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
+  }
+  if (p.lse && lane == 0) p.lse[orow * p.Hq + kv * p.G + g] = L == 0.0f ? -INFINITY : M + logf(L);
+}
+
+template <int D>
+cudaError_t launch_any(const TreeParams& p, cudaStream_t s) {
+  const int rc = row_chunks(D, p.c.r);
+  const size_t smem = 16 * (static_cast<size_t>(kRT + kTT) * rc + kTT * (D / 4)) + 4 * kRT * (kTT + 1);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(tree_any_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  dim3 grid((p.span.n * p.G + kRT - 1) / kRT, p.splits, p.c.B * p.c.Hkv);
+  tree_any_kernel<D><<<grid, kThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_merge(const TreeParams& p, cudaStream_t s) {
+  dim3 grid((p.span.n * p.G + 3) / 4, p.c.B * p.c.Hkv);
+  tree_merge_kernel<D><<<grid, 128, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Splits of the fp32 kernel: about four CTAs per SM, chunks of whole 32-token tiles.
+TreePlan tree_plan(const headq_cache& c, int Hq, int n, int T, bool q_bf16) {
+  (void)q_bf16;
+  TreePlan tp{1, kTT};
+  if (T <= 0 || n <= 0 || c.B <= 0) return tp;
+  const long long units = static_cast<long long>(c.B) * c.Hkv * ((static_cast<long long>(n) * (Hq / c.Hkv) + kRT - 1) / kRT);
+  long long s = 4ll * sm_count() / units;
+  const int tiles = (T + kTT - 1) / kTT;
+  s = s < 1 ? 1 : (s > 64 ? 64 : s);
+  if (s > tiles) s = tiles;
+  const int per = static_cast<int>((tiles + s - 1) / s);
+  tp.chunk = per * kTT;
+  tp.splits = (tiles + per - 1) / per;
+  return tp;
+}
+
+cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
+  cudaError_t e = cudaErrorInvalidValue;
+#define HEADQ_TREE_D(D)                                              \
+  case D:                                                            \
+    e = launch_any<D>(p, s);                                         \
+    if (e == cudaSuccess && p.splits > 1) e = launch_merge<D>(p, s); \
+    break;
+  switch (p.c.d) {
+    HEADQ_TREE_D(8)
+    HEADQ_TREE_D(16)
+    HEADQ_TREE_D(32)
+    HEADQ_TREE_D(64)
+    HEADQ_TREE_D(128)
+    HEADQ_TREE_D(256)
+  }
+#undef HEADQ_TREE_D
+  return e;
+}
+
+}  // namespace headq

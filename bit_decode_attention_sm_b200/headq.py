@@ -7,8 +7,10 @@ fallback: without the built library, or with tensors that are not on a CUDA
 device, every call raises.
 
 Names follow the C ABI: :func:`headq_calibrate`, :func:`headq_cache_write`,
-:func:`headq_decode_attn`, :func:`headq_attn_kl`, plus :class:`HeadQCache`
-which owns the packed cache planes.
+:func:`headq_decode_attn`, :func:`headq_attn_kl`, the packed-batch calls
+:func:`headq_cache_write_ragged`, :func:`headq_cache_read` and
+:func:`headq_tree_attn`, plus :class:`HeadQCache` which owns the packed cache
+planes.
 """
 
 import ctypes
@@ -33,7 +35,8 @@ EXPORTS = ("headq_version", "headq_status_string", "headq_calibrate",
            "headq_decode_attn_noalloc", "headq_decode_noalloc_status",
            "headq_decode_append", "headq_shard_seq_lens",
            "headq_merge_partials", "headq_a2_workspace_bytes", "headq_a2_scores",
-           "headq_a2_select", "headq_a2_value_fixup")
+           "headq_a2_select", "headq_a2_value_fixup", "headq_cache_write_ragged",
+           "headq_cache_read", "headq_tree_attn", "headq_tree_workspace_bytes")
 
 
 KMODES = {"token": 0, "channel": 1}  # headq_kmode
@@ -60,6 +63,18 @@ class CacheStruct(ctypes.Structure):
                 ("kmode", ctypes.c_int)]
 
 
+class SpanStruct(ctypes.Structure):
+    """Mirror of ``headq_span``."""
+    _fields_ = [("seq_lens", ctypes.c_void_p), ("cu", ctypes.c_void_p), ("T", ctypes.c_int),
+                ("n", ctypes.c_int), ("rows", ctypes.c_int)]
+
+
+class RowsStruct(ctypes.Structure):
+    """Mirror of ``headq_rows``."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
 _lib = None
 
 
@@ -73,7 +88,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         F = ctypes.c_float
-        CP = ctypes.POINTER(CacheStruct)
+        CP, SP, RP = (ctypes.POINTER(c) for c in (CacheStruct, SpanStruct, RowsStruct))
         sig = {
             "headq_version": ([], I),
             "headq_status_string": ([I], ctypes.c_char_p),
@@ -95,6 +110,10 @@ def lib():
             "headq_a2_scores": ([CP, P, I, I, I, P, I, P, P, I, F, P, P, Z, P], I),
             "headq_a2_select": ([P, I, I, P, I, I, P, I, I, P, P, P], I),
             "headq_a2_value_fixup": ([CP, P, I, I, P, I, P, F, I, P, P, I, I, P, P, P], I),
+            "headq_cache_write_ragged": ([CP, RP, RP, I, P, SP, P, P], I),
+            "headq_cache_read": ([CP, SP, P, I, RP, RP, P, P], I),
+            "headq_tree_attn": ([CP, RP, I, P, ctypes.c_longlong, SP, P, F, I, RP, P, P, Z, P], I),
+            "headq_tree_workspace_bytes": ([CP, I, I, I], Z),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -182,6 +201,59 @@ class HeadQCache:
         else:
             raise ValueError("vmode is 'dense' or '2bit'")
 
+    @staticmethod
+    def from_planes(k_codes, k_scale, k_min, z_codes=None, z_scale=None, v=None, v_codes=None,
+                    v_scale=None, v_min=None, kmode="token", block_table=None):
+        """A cache over planes that are allocated already (a server's pools): contiguous
+        CUDA tensors laid out as the class says, nothing copied.  With ``block_table``
+        (int32 [B, max_pages]) the planes are pools of pages and the result is a
+        :class:`PagedHeadQCache`.  z_codes/z_scale None: rank 0."""
+        lead, d = tuple(k_codes.shape[:3]), k_codes.shape[3] * 4
+        r = 0 if z_codes is None else z_codes.shape[3] * 2
+        ng = d // min(32, d)
+        if kmode not in KMODES:
+            raise ValueError("kmode is 'token' or 'channel'")
+        if (v is None) == (v_codes is None):
+            raise ValueError("either v (dense values) or v_codes, v_scale and v_min")
+        u8, f32 = torch.uint8, torch.float32
+        sshape = lead + (ng,) if kmode == "token" else lead[:2] + (lead[2] // 64, d)
+        want = dict(k_codes=(k_codes, u8, lead + (d // 4,)), k_scale=(k_scale, f32, sshape),
+                    k_min=(k_min, f32, sshape))
+        if r:
+            want.update(z_codes=(z_codes, u8, lead + (r // 2,)), z_scale=(z_scale, f32, lead))
+        if v is None:
+            want.update(v_codes=(v_codes, u8, lead + (d // 4,)), v_scale=(v_scale, f32, lead + (ng,)),
+                        v_min=(v_min, f32, lead + (ng,)))
+        else:
+            _dtype_code(v)
+            want.update(v=(v, v.dtype, lead + (d,)))
+        for name, (t, dt, shape) in want.items():
+            if _cuda(t, name) is None or t.dtype != dt or tuple(t.shape) != shape:
+                raise ValueError("%s must be %s %s" % (name, dt, list(shape)))
+            if t.device != k_codes.device:
+                raise ValueError("%s is on %s, k_codes on %s" % (name, t.device, k_codes.device))
+        if block_table is None:
+            c = HeadQCache.__new__(HeadQCache)
+            c.B, c.T_cap = lead[0], lead[2]
+            if c.T_cap % (64 if kmode == "channel" else 16):
+                raise ValueError("T_cap must be a multiple of 16 (64 for per-channel keys)")
+        else:
+            c = PagedHeadQCache.__new__(PagedHeadQCache)
+            if _cuda(block_table, "block_table").dtype != torch.int32 or block_table.dim() != 2:
+                raise ValueError("block_table must be int32 [B, max_pages]")
+            c.B, c.max_pages = block_table.shape
+            c.num_pages, c.page_size = lead[0], lead[2]
+            if c.page_size <= 0 or c.page_size % 64:
+                raise ValueError("page_size must be a positive multiple of 64")
+            c.T_cap = c.max_pages * c.page_size
+            c.block_table = block_table
+        c.Hkv, c.d, c.r, c.kmode = lead[1], d, r, kmode
+        c.vmode = "dense" if v_codes is None else "2bit"
+        c.v_dtype = torch.bfloat16 if v is None else v.dtype
+        c.k_codes, c.k_scale, c.k_min, c.z_codes, c.z_scale = k_codes, k_scale, k_min, z_codes, z_scale
+        c.v, c.v_codes, c.v_scale, c.v_min = v, v_codes, v_scale, v_min
+        return c
+
     def planes(self):
         out = dict(kc=self.k_codes, ks=self.k_scale, km=self.k_min, zc=self.z_codes,
                    zs=self.z_scale)
@@ -209,8 +281,9 @@ class HeadQCache:
         s.k_codes = self.k_codes.data_ptr()
         s.k_scale = self.k_scale.data_ptr()
         s.k_min = self.k_min.data_ptr()
-        s.z_codes = self.z_codes.data_ptr()
-        s.z_scale = self.z_scale.data_ptr()
+        if self.z_codes is not None:
+            s.z_codes = self.z_codes.data_ptr()
+            s.z_scale = self.z_scale.data_ptr()
         if self.vmode == "dense":
             s.v = self.v.data_ptr()
         else:
@@ -463,6 +536,179 @@ def headq_a2_value_fixup(cache, q, U, keep_idx, keep_v, out, lse, T=None, seq_le
         ctypes.byref(cs), _ptr(q), _dtype_code(q), Hq, _ptr(seq_lens), T, _ptr(U),
         ctypes.c_float(sm), int(corr_sign), _ptr(keep_idx), _ptr(keep_v), _dtype_code(keep_v),
         keep_idx.shape[-1], _ptr(out), _ptr(lse), _stream(stream)))
+    return out
+
+
+def _same_device(cache, **tensors):
+    """The cache's device, on which every tensor of a call must be."""
+    dev = cache.k_codes.device
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError("%s is on %s, the cache on %s" % (name, t.device, dev))
+    return dev
+
+
+def _rows(t, name, heads, d, written=False):
+    """``headq_rows`` of a packed tensor [rows, heads, d]: any row and head strides that are
+    multiples of 16 bytes, channels contiguous; elements of a written one do not overlap."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError("%s must be [rows, %d, %d], got %s" % (name, heads, d, list(t.shape)))
+    code = _dtype_code(t)
+    rs, hs, cs = t.stride()
+    per = 4 if code == HEADQ_F32 else 8
+    if t.shape[0] <= 1:  # the strides of a single row or head are never used
+        rs = 0
+    if heads == 1:
+        hs = 0
+    if cs != 1 or rs % per or hs % per:
+        raise ValueError("%s: channels must be contiguous and the other strides multiples of 16 bytes"
+                         % name)
+    if written and t.shape[0] > 1 and heads > 0:
+        lo, hi = sorted(((rs, t.shape[0]), (hs, heads))) if heads > 1 else ((d, 1), (rs, t.shape[0]))
+        if lo[0] < d or hi[0] < (lo[1] - 1) * lo[0] + d:
+            raise ValueError("%s: its rows and heads overlap" % name)
+    elif written and heads > 1 and hs < d:
+        raise ValueError("%s: its rows and heads overlap" % name)
+    return RowsStruct(t.data_ptr(), code, rs, hs)
+
+
+def _int32(t, name, shape):
+    if t is None:
+        return None
+    if _cuda(t, name).dtype != torch.int32 or tuple(t.shape) != shape:
+        raise ValueError("%s must be int32 %s" % (name, list(shape)))
+    return t.data_ptr()
+
+
+def _span(cache, seq_lens, cu, n, T, rows):
+    """``headq_span`` of a packed batch of `rows` rows."""
+    if n is None:
+        if cu is not None:
+            raise ValueError("n (the most rows of one sequence) is needed with cu")
+        if cache.B and rows % cache.B:
+            raise ValueError("%d rows are no whole number for each of %d sequences" % (rows, cache.B))
+        n = rows // cache.B if cache.B else 0
+    return SpanStruct(_int32(seq_lens, "seq_lens", (cache.B,)), _int32(cu, "cu", (cache.B + 1,)),
+                      cache.T_cap if T is None else int(T), int(n), rows)
+
+
+def _basis(cache, U):
+    if cache.r == 0:
+        return None
+    if _cuda(U, "U") is None or U.dtype != torch.float32 or tuple(U.shape) != (cache.Hkv, cache.d, cache.r):
+        raise ValueError("U must be float32 [%d, %d, %d]" % (cache.Hkv, cache.d, cache.r))
+    return U.data_ptr()
+
+
+def _stream_on(dev, stream):
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+
+
+def headq_cache_write_ragged(cache, k, v, U, seq_lens=None, cu=None, n=None, T=None, src=None,
+                             stream=None):
+    """Encode a packed batch of new tokens, k and v [rows, Hkv, d] (v None: values left as
+    they are), into the last cached positions of every sequence.
+
+    Sequence b's tokens are rows cu[b] .. cu[b+1] (cu None: n rows each, n = rows / B);
+    they lie at positions T_b - n_b .. T_b - 1, T_b = seq_lens[b] (None: T, or the capacity).
+    n: the most rows of one sequence.  src (int32 [rows]): row r takes its token from row
+    src[r] of k and v.  Strided k and v (slices of a fused projection) need no copy."""
+    ks = _rows(k, "k", cache.Hkv, cache.d)
+    vs = None if v is None else _rows(v, "v", cache.Hkv, cache.d)
+    if v is not None and (v.dtype != k.dtype or v.shape[0] != k.shape[0]):
+        raise ValueError("k and v must have the same dtype and rows")
+    rows = k.shape[0] if src is None else src.shape[0]
+    dev = _same_device(cache, k=k, v=v, U=U, seq_lens=seq_lens, cu=cu, src=src)
+    sp = _span(cache, seq_lens, cu, n, T, rows)
+    cs = cache.struct()
+    with torch.cuda.device(dev):
+        _check("headq_cache_write_ragged", lib().headq_cache_write_ragged(
+            cs, ks, vs, k.shape[0], _int32(src, "src", (rows,)), sp, _basis(cache, U),
+            _stream_on(dev, stream)))
+
+
+def headq_cache_read(cache, U, seq_lens=None, cu=None, n=None, T=None, rows=None, corr_sign=1,
+                     dtype=torch.bfloat16, k_out=None, v_out=None, ws=None, stream=None):
+    """Decode cached tokens to dense (k, v), each [rows, Hkv, d]: the key the corrected logit
+    reads and the cached value.  The tokens are named as in :func:`headq_cache_write_ragged`;
+    any interval [a, e) of a sequence is T_b = e with n_b = e - a.  Give k_out and/or v_out
+    (strided rows are fine; only what is given is computed), or neither, for new tensors of
+    `dtype` with `rows` rows (B * n where there is no cu).  ws: a decode or tree workspace
+    whose error word a block-table entry outside the pool sets."""
+    if k_out is None and v_out is None:
+        if rows is None:
+            if cu is not None or n is None:
+                raise ValueError("rows is needed (with cu), or n")
+            rows = cache.B * n
+        shape = (rows, cache.Hkv, cache.d)
+        k_out, v_out = (torch.zeros(shape, dtype=dtype, device=cache.k_codes.device) for _ in "kv")
+    have = [t.shape[0] for t in (k_out, v_out) if t is not None]
+    if len(set(have)) > 1 or (rows is not None and rows != have[0]):
+        raise ValueError("k_out and v_out must have the same rows")
+    ks = None if k_out is None else _rows(k_out, "k_out", cache.Hkv, cache.d, True)
+    vs = None if v_out is None else _rows(v_out, "v_out", cache.Hkv, cache.d, True)
+    dev = _same_device(cache, k_out=k_out, v_out=v_out, U=U, seq_lens=seq_lens, cu=cu, ws=ws)
+    sp = _span(cache, seq_lens, cu, n, T, have[0])
+    cs = cache.struct()
+    with torch.cuda.device(dev):
+        _check("headq_cache_read", lib().headq_cache_read(
+            cs, sp, None if k_out is None else _basis(cache, U), int(corr_sign), ks, vs,
+            None if ws is None else ws.data_ptr(), _stream_on(dev, stream)))
+    return k_out, v_out
+
+
+def tree_workspace(cache, Hq, n, T=None):
+    """A zeroed device workspace for headq_tree_attn with up to n new tokens per sequence."""
+    cs = cache.struct()
+    with torch.cuda.device(cache.k_codes.device):
+        nb = lib().headq_tree_workspace_bytes(cs, Hq, int(n), cache.T_cap if T is None else int(T))
+    return torch.zeros(max(nb, 256), dtype=torch.uint8, device=cache.k_codes.device)
+
+
+def headq_tree_attn(cache, q, U, mask=None, seq_lens=None, cu=None, n=None, T=None, sm_scale=None,
+                    corr_sign=1, out=None, lse=None, ws=None, stream=None):
+    """Attention of a packed batch of new tokens q [rows, Hq, d] over the cache, which holds
+    those tokens already; returns out [rows, Hq, d] of q's dtype.
+
+    The tokens are named as in :func:`headq_cache_write_ragged`.  New token i of a sequence
+    sees all tokens before its sequence's new ones, and new token j where mask[i, j] (bool or
+    uint8 [n, n], one tree for all, or [B, n, n]); mask None: j <= i.  A row that sees nothing
+    gives 0.  lse: fp32 [rows, Hq], written when given.  Rows of no sequence keep what `out`
+    holds (zeros when it is allocated here)."""
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, Hq, %d], got %s" % (cache.d, list(q.shape)))
+    rows, Hq = q.shape[:2]
+    if Hq == 0 or Hq % cache.Hkv:
+        raise ValueError("Hq must be a multiple of Hkv")
+    if out is None:
+        out = torch.zeros((rows, Hq, cache.d), dtype=q.dtype, device=q.device)
+    qs, os_ = _rows(q, "q", Hq, cache.d), _rows(out, "out", Hq, cache.d, True)
+    if out.shape[0] != rows or out.dtype != q.dtype:
+        raise ValueError("out must have q's rows and dtype")
+    if lse is not None and (_cuda(lse, "lse").dtype != torch.float32 or tuple(lse.shape) != (rows, Hq)):
+        raise ValueError("lse must be float32 [%d, %d]" % (rows, Hq))
+    dev = _same_device(cache, q=q, out=out, U=U, mask=mask, seq_lens=seq_lens, cu=cu, lse=lse, ws=ws)
+    sp = _span(cache, seq_lens, cu, n, T, rows)
+    mp, ms = None, 0
+    if mask is not None:
+        if _cuda(mask, "mask").dtype not in (torch.bool, torch.uint8):
+            raise TypeError("mask must be bool or uint8")
+        if tuple(mask.shape) == (cache.B, sp.n, sp.n):
+            ms = sp.n * sp.n
+        elif tuple(mask.shape) != (sp.n, sp.n):
+            raise ValueError("mask must be [%d, %d] or [%d, %d, %d]" % (sp.n, sp.n, cache.B, sp.n, sp.n))
+        mp = mask.data_ptr()
+    if ws is None:
+        ws = tree_workspace(cache, Hq, sp.n, sp.T)
+    sm = 1.0 / math.sqrt(cache.d) if sm_scale is None else float(sm_scale)
+    cs = cache.struct()
+    with torch.cuda.device(dev):
+        _check("headq_tree_attn", lib().headq_tree_attn(
+            cs, qs, Hq, mp, ms, sp, _basis(cache, U), sm, int(corr_sign), os_,
+            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
+            _stream_on(dev, stream)))
     return out
 
 

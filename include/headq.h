@@ -33,8 +33,8 @@
  *     scale = (mx - mn) / 3, code = clamp(rint((x - mn) / scale), 0, 3) with
  *     round-half-even (all codes 0 when scale == 0); the residual is
  *     e = x - (mn + code*scale) (product rounded first); the projection
- *     y = U_h^T e accumulates channel by channel in order with one fused
- *     multiply-add per term; the side scale is s = max|y| / 7 and the side code
+ *     y = U_h^T e accumulates channel by channel in order, each term a
+ *     rounded product and then a rounded sum; the side scale is s = max|y| / 7 and the side code
  *     w = clamp(rint(y / s), -7, 7) (all 0 when s == 0).  Every operation is one
  *     IEEE fp32 operation (division correctly rounded, no flush-to-zero).
  */
@@ -383,6 +383,99 @@ headq_status headq_shard_seq_lens(const int32_t *seq_lens, int B, int T, int t_l
 headq_status headq_merge_partials(const float *o_parts, const float *lse_parts, int S, int BH,
                                   int d, size_t part_stride, float *out, float *lse,
                                   headq_stream_t stream);
+
+/*
+ * Packed batches of new tokens: prefill chunks, drafts of speculative decoding
+ * and single tokens in one call, each sequence at its own positions.
+ *
+ * headq_span names the tokens of a call: for every sequence b, its last n_b cached
+ * tokens.  They are rows [cu[b], cu[b+1]) of the call's packed tensors, in order;
+ * row cu[b] + i is cached position T_b - n_b + i.  (The same rule as
+ * headq_decode_append, where the one new token of a sequence lies at T_b - 1.)
+ *   seq_lens  int32 [B] (device, nullable): T_b, clamped to [0, T]; NULL: T_b = T.
+ *   cu        int32 [B+1] (device, nullable): first row of each sequence, ascending;
+ *             NULL: n rows each, cu[b] = b * n (then rows >= B * n).
+ *   n         most rows of one sequence (n_b <= n: rows past n are not part of the call).
+ *   rows      rows of the packed tensors.  Rows that belong to no sequence are left as
+ *             they were.  A sequence with cu[b] < 0, cu[b+1] < cu[b] or cu[b+1] > rows
+ *             has n_b = 0.  One with n_b > T_b takes no part: nothing is written to
+ *             the cache, headq_cache_read leaves its rows as they were, and in
+ *             headq_tree_attn its rows see nothing.
+ *
+ * headq_rows is a packed tensor [rows, heads, d]: element strides between rows and
+ * between heads, channels contiguous.  ptr is 16-byte aligned and both strides are
+ * multiples of 16 bytes (of 8 bf16 or 4 fp32 elements): a slice of a fused projection's
+ * output needs no copy.
+ */
+typedef struct {
+    const int32_t *seq_lens;
+    const int32_t *cu;
+    int T, n, rows;
+} headq_span;
+
+typedef struct {
+    void *ptr;
+    headq_dtype dtype;
+    long long row_stride, head_stride;
+} headq_rows;
+
+/*
+ * headq_cache_write_ragged -- encode the new tokens of a packed batch into the cache
+ * (the per-token code of headq_cache_write, bit for bit; summary section 3, step 2).
+ *   k, v  [src_rows, Hkv, d], one dtype; v nullable (V is then left untouched).
+ *   src   int32 [rows] (device, nullable): packed row r takes its token from row
+ *         src[r] of k and v -- the accepted nodes of a draft tree, say; a token whose
+ *         src lies outside [0, src_rows) is not written.  NULL: row r itself
+ *         (src_rows == rows).
+ * A block-table entry outside the page pool drops the token.  Two rows of one call
+ * never share a cache position.  HEADQ_K_TOKEN caches only (per-channel key blocks
+ * are sealed once written).
+ */
+headq_status headq_cache_write_ragged(const headq_cache *cache, const headq_rows *k,
+                                      const headq_rows *v, int src_rows, const int32_t *src,
+                                      const headq_span *span, const float *U,
+                                      headq_stream_t stream);
+
+/*
+ * headq_cache_read -- decode cached tokens to dense rows (summary section 3: the key
+ * the corrected logit reads, and the cached value):
+ *   k_out[row, kv] = k^base + corr_sign * U_h z^ ,  v_out[row, kv] = v^
+ * computed in fp32 and rounded once to the rows' dtype.  k_out or v_out may be NULL.
+ * Any interval [a, e) of a sequence is the span with T_b = e and n_b = e - a.  Both key
+ * codes are supported.  A block-table entry outside the page pool gives zero rows, and
+ * sets the error word of `ws` when there is one (ws nullable: any zero-filled decode or
+ * tree workspace; only its first word is used).
+ */
+headq_status headq_cache_read(const headq_cache *cache, const headq_span *span, const float *U,
+                              int corr_sign, const headq_rows *k_out, const headq_rows *v_out,
+                              void *ws, headq_stream_t stream);
+
+/*
+ * headq_tree_attn -- attention of several new tokens per sequence over the cache: the
+ * verification pass of speculative decoding, with the drafted tokens already encoded
+ * in the cache (headq_cache_write_ragged) as a tree.  Row i of sequence b sees every
+ * token j < P_b = T_b - n_b, and of its n_b new tokens those with mask[b, i, j - P_b]:
+ *   s^_j = sm_scale * ( q.k^base_j + corr_sign * (U_h^T q) . z^_j )
+ *   out[row, h] = sum_j softmax(s^)_j v^_j ,  lse[row, h] = log sum_j exp(s^_j)
+ * over the tokens it sees, as headq_decode_attn computes them for a path through the
+ * tree: what a token's keys and values hold does not reach a row that does not see it.
+ * A row that sees nothing gets out = 0, lse = -inf.
+ *   q     [rows, Hq, d];  out  [rows, Hq, d] of q's dtype;  lse fp32 [rows, Hq] (nullable)
+ *   mask  uint8 [n, n] of sequence b at mask + b * mask_stride bytes, row i column j
+ *         nonzero when new token i sees new token j (mask_stride 0: one tree for all).
+ *         NULL: j <= i, a plain run of new tokens (mask_stride is then ignored).
+ *   ws    headq_tree_workspace_bytes(...) bytes, zero-filled before first use; its first
+ *         word is the device error word.  Calls sharing it must not overlap on the GPU.
+ * bf16 q with bf16 or 2-bit values, d 64 or 128 and r 0, 8 or 16 runs on the tensor cores:
+ * keys are rounded to 11 bits relative to the largest of their tile and softmax weights
+ * to bf16, so out carries about 2 roundings to bf16.  Every other shape, and fp32 q, is
+ * computed in fp32.  HEADQ_K_TOKEN caches only.
+ */
+headq_status headq_tree_attn(const headq_cache *cache, const headq_rows *q, int Hq,
+                             const uint8_t *mask, long long mask_stride, const headq_span *span,
+                             const float *U, float sm_scale, int corr_sign, const headq_rows *out,
+                             float *lse, void *ws, size_t ws_bytes, headq_stream_t stream);
+size_t headq_tree_workspace_bytes(const headq_cache *cache, int Hq, int n, int T);
 
 /*
  * headq_workspace_status -- waits for `stream`, reads the device error word of a
