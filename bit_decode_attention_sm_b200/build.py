@@ -27,7 +27,7 @@ LIB = os.path.join(PKG, "libheadq.so")
 
 SOURCES = ["headq_api.cu", "cache_write.cu", "decode_attn.cu", "attn_kl.cu",
            "calibrate.cu", "decode_noalloc.cu", "decode_mma.cu", "decode_hm.cu", "attn_kl_hm.cu", "merge.cu",
-           "a2_policy.cu", "cache_write_ragged.cu", "cache_read.cu", "tree_attn.cu", "packed_api.cu"]
+           "a2_policy.cu", "cache_write_ragged.cu", "cache_read.cu", "tree_attn.cu", "tree_mma.cu", "packed_api.cu"]
 PER_FILE_FLAGS = {"cache_write.cu": ["-fmad=false"], "cache_write_ragged.cu": ["-fmad=false"]}
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",

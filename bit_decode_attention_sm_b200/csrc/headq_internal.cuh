@@ -162,7 +162,7 @@ struct CacheReadParams {
 
 // headq_tree_attn.  Query row x = i * G + g of a (b, kv) unit: new token i, query head
 // kv * G + g.  Partials of a T-split: o [unit][split][n * G][d] unnormalised, then
-// (running max in natural-log units, sum) [unit][split][n * G].
+// (running max in natural-log units, sum, sum for the log-sum-exp, 0) [unit][split][n * G].
 struct TreeParams {
   headq_cache c;
   headq_rows q, out;
@@ -176,7 +176,7 @@ struct TreeParams {
   float* lse;
   int splits, chunk;
   float* part_o;
-  float2* part_ml;
+  float4* part_ml;
   unsigned* err;
 };
 

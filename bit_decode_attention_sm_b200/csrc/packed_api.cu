@@ -27,13 +27,21 @@ headq_status check_rows(const headq_rows* r) {
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-size_t part_rows(const headq_cache& c, int Hq, int n, const TreePlan& tp) {
-  return tp.splits > 1 ? static_cast<size_t>(c.B) * Hq * n * tp.splits : 0;
-}
-
-size_t tree_ws(const headq_cache& c, int Hq, int n, int T, bool q_bf16) {
-  const size_t rows = part_rows(c, Hq, n, tree_plan(c, Hq, n, T, q_bf16));
-  return kWsHeaderBytes + round256(rows * c.d * sizeof(float)) + round256(rows * sizeof(float2));
+// Tree workspace: [error word][partial outputs][partial statistics][query images][logit
+// factors][mask bits], the last three for the tensor-core kernel
+struct TreeWs {
+  size_t part_ml, qimg, qf, words, bytes;
+};
+TreeWs tree_ws(const headq_cache& c, int Hq, int n, const TreePlan& tp) {
+  TreeWs w{};
+  const size_t units = static_cast<size_t>(c.B) * c.Hkv;
+  const size_t rows = tp.parts > 1 ? static_cast<size_t>(c.B) * Hq * n * tp.parts : 0;
+  w.part_ml = kWsHeaderBytes + round256(rows * c.d * sizeof(float));
+  w.qimg = w.part_ml + round256(rows * sizeof(float4));
+  w.qf = w.qimg + (tp.mma ? round256(units * tp.blocks * tree_mma_image_bytes(c)) : 0);
+  w.words = w.qf + (tp.mma ? round256(units * tp.blocks * 128 * sizeof(float)) : 0);
+  w.bytes = w.words + (tp.mma ? round256(static_cast<size_t>(c.B) * n * ((n + 31) / 32) * 4) : 0);
+  return w;
 }
 
 }  // namespace
@@ -102,7 +110,8 @@ HEADQ_API headq_status headq_cache_read(const headq_cache* cache, const headq_sp
 
 HEADQ_API size_t headq_tree_workspace_bytes(const headq_cache* cache, int Hq, int n, int T) {
   if (check_cache(cache) != HEADQ_OK || Hq <= 0 || Hq % cache->Hkv || n < 0 || T < 0) return 0;
-  const size_t a = tree_ws(*cache, Hq, n, T, true), b = tree_ws(*cache, Hq, n, T, false);
+  const size_t a = tree_ws(*cache, Hq, n, tree_plan(*cache, Hq, n, T, true)).bytes;
+  const size_t b = tree_ws(*cache, Hq, n, tree_plan(*cache, Hq, n, T, false)).bytes;
   return a > b ? a : b;  // the queries' dtype is not known here
 }
 
@@ -127,9 +136,9 @@ HEADQ_API headq_status headq_tree_attn(const headq_cache* cache, const headq_row
   if (out->dtype != q->dtype) return HEADQ_ERR_INVALID_ARG;
   if (cache->r > 0 && (!U || !aligned16(U))) return HEADQ_ERR_INVALID_ARG;
   const bool qb = q->dtype == HEADQ_BF16;
-  if (!ws || !aligned16(ws) || ws_bytes < tree_ws(*cache, Hq, span->n, span->T, qb))
-    return HEADQ_ERR_WORKSPACE;
   const TreePlan tp = tree_plan(*cache, Hq, span->n, span->T, qb);
+  const TreeWs w = tree_ws(*cache, Hq, span->n, tp);
+  if (!ws || !aligned16(ws) || ws_bytes < w.bytes) return HEADQ_ERR_WORKSPACE;
   TreeParams p{};
   p.c = *cache;
   p.q = *q;
@@ -143,14 +152,19 @@ HEADQ_API headq_status headq_tree_attn(const headq_cache* cache, const headq_row
   p.sm_scale = sm_scale;
   p.corr_sign = static_cast<float>(corr_sign);
   p.lse = lse;
-  p.splits = tp.splits;
+  p.splits = tp.parts;
   p.chunk = tp.chunk;
-  char* w = static_cast<char*>(ws);
-  p.err = reinterpret_cast<unsigned*>(w);
-  p.part_o = reinterpret_cast<float*>(w + kWsHeaderBytes);
-  p.part_ml = reinterpret_cast<float2*>(
-      w + kWsHeaderBytes +
-      round256(part_rows(*cache, Hq, span->n, tp) * cache->d * sizeof(float)));
-  return launch_tree(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? HEADQ_OK
-                                                                              : HEADQ_ERR_CUDA;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  p.err = reinterpret_cast<unsigned*>(base);
+  p.part_o = reinterpret_cast<float*>(base + kWsHeaderBytes);
+  p.part_ml = reinterpret_cast<float4*>(base + w.part_ml);
+  TreeMma t{};
+  t.qimg = base + w.qimg;
+  t.qf = reinterpret_cast<float*>(base + w.qf);
+  t.words = mask ? reinterpret_cast<uint32_t*>(base + w.words) : nullptr;
+  t.wpr = (span->n + 31) / 32;
+  t.blocks = tp.blocks;
+  return launch_tree(p, t, tp, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? HEADQ_OK
+             : HEADQ_ERR_CUDA;
 }

@@ -5,12 +5,28 @@
 
 namespace headq {
 
-// T-splits per (sequence, KV head) and tokens per split
+// How a call runs: on the tensor cores (tree_mma.cu) with one or (pair) two 128-row blocks
+// per CTA, or in fp32 (tree_attn.cu); grid_splits T-splits of `chunk` tokens per (sequence,
+// KV head), which leave `parts` partial results to merge (1: none).
 struct TreePlan {
-  int splits, chunk;
+  bool mma, pair;
+  int blocks, grid_splits, parts, chunk;
 };
 TreePlan tree_plan(const headq_cache& c, int Hq, int n, int T, bool q_bf16);
-cudaError_t launch_tree(const TreeParams& p, cudaStream_t s);
+
+// Operands of the tensor-core kernel in the workspace: shared-memory images of the query
+// rows [unit][block], each row's logit factor [unit][block * 128], mask bits [B][n][wpr]
+// (null without a mask).
+struct TreeMma {
+  uint8_t* qimg;
+  float* qf;
+  uint32_t* words;
+  int wpr, blocks;
+};
+bool tree_mma_supported(const headq_cache& c);
+size_t tree_mma_image_bytes(const headq_cache& c);
+cudaError_t launch_tree_mma(const TreeParams& p, const TreeMma& t, int grid_splits, bool pair, cudaStream_t s);
+cudaError_t launch_tree(const TreeParams& p, const TreeMma& t, const TreePlan& plan, cudaStream_t s);
 
 // whether new token i of sequence b sees its new token j (both below span.n)
 __device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int i, int j) {

@@ -196,7 +196,7 @@ tree_any_kernel(const TreeParams p) {
 #pragma unroll
     for (int k = 0; k < NC; ++k)
       if (l8 + 8 * k < D / 4) reinterpret_cast<float4*>(p.part_o + pr * D)[l8 + 8 * k] = acc[k];
-    if (l8 == 0) p.part_ml[pr] = make_float2(m, l);
+    if (l8 == 0) p.part_ml[pr] = make_float4(m, l, l, 0.0f);
     return;
   }
   const int i = x / p.G, g = x - i * p.G;
@@ -229,15 +229,16 @@ tree_merge_kernel(const TreeParams p) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float base = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f;
+  float L = 0.0f, Lx = 0.0f;
   float4 acc[NC];
 #pragma unroll
   for (int k = 0; k < NC; ++k) acc[k] = make_float4(0, 0, 0, 0);
 #pragma unroll 4
   for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = p.part_ml[pr + s * ru];
+    const float4 ml = p.part_ml[pr + s * ru];
     const float w = exp2f((ml.x - base) * kLog2e);
     L = fmaf(w, ml.y, L);
+    Lx = fmaf(w, ml.z, Lx);
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       if (lane + 32 * k >= D / 4) continue;
@@ -260,7 +261,7 @@ tree_merge_kernel(const TreeParams p) {
     store_row4(p.out, orow * p.out.row_stride + (kv * p.G + g) * p.out.head_stride + 4 * c4,
                make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
   }
-  if (p.lse && lane == 0) p.lse[orow * p.Hq + kv * p.G + g] = L == 0.0f ? -INFINITY : M + logf(L);
+  if (p.lse && lane == 0) p.lse[orow * p.Hq + kv * p.G + g] = L == 0.0f ? -INFINITY : M + logf(Lx);
 }
 
 template <int D>
@@ -286,24 +287,50 @@ cudaError_t launch_merge(const TreeParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// Splits of the fp32 kernel: about four CTAs per SM, chunks of whole 32-token tiles.
+// Tensor cores: one CTA per SM, so the splits that minimise waves x (tiles per CTA + 3),
+// the 3 standing for a CTA's set-up, first loads and epilogue.  fp32 kernel: about four
+// CTAs per SM, chunks of whole 32-token tiles.
 TreePlan tree_plan(const headq_cache& c, int Hq, int n, int T, bool q_bf16) {
-  (void)q_bf16;
-  TreePlan tp{1, kTT};
-  if (T <= 0 || n <= 0 || c.B <= 0) return tp;
-  const long long units = static_cast<long long>(c.B) * c.Hkv * ((static_cast<long long>(n) * (Hq / c.Hkv) + kRT - 1) / kRT);
-  long long s = 4ll * sm_count() / units;
-  const int tiles = (T + kTT - 1) / kTT;
+  const long long units = static_cast<long long>(c.B) * c.Hkv, rows = static_cast<long long>(n) * (Hq / c.Hkv);
+  TreePlan tp{q_bf16 && tree_mma_supported(c), false, static_cast<int>((rows + 127) / 128), 1, 1, 128};
+  if (n <= 0 || units <= 0) return tp;
+  const int sms = sm_count();
+  if (tp.mma) {
+    tp.pair = tp.blocks > 1;
+    const long long ctas = units * (tp.pair ? (tp.blocks + 1) / 2 : tp.blocks);
+    const int tiles = T > 128 ? (T + 127) / 128 : 1;
+    long long best = -1;
+    for (int s = 1; s <= tiles && s <= sms; ++s) {
+      const int per = (tiles + s - 1) / s, used = (tiles + per - 1) / per;
+      if (used != s) continue;
+      const long long cost = ((ctas * s + sms - 1) / sms) * (per + 3) + (s > 1 ? 1 : 0);
+      if (best < 0 || cost < best) {
+        best = cost;
+        tp.grid_splits = s;
+        tp.chunk = per * 128;
+      }
+    }
+    // the two lanes of a CTA that take alternate tiles end as two parts
+    tp.parts = tp.grid_splits * (!tp.pair && tp.chunk > 128 ? 2 : 1);
+    return tp;
+  }
+  const int tiles = T > kTT ? (T + kTT - 1) / kTT : 1;
+  long long s = 4ll * sms / (units * ((rows + kRT - 1) / kRT));
   s = s < 1 ? 1 : (s > 64 ? 64 : s);
   if (s > tiles) s = tiles;
   const int per = static_cast<int>((tiles + s - 1) / s);
   tp.chunk = per * kTT;
-  tp.splits = (tiles + per - 1) / per;
+  tp.grid_splits = tp.parts = (tiles + per - 1) / per;
   return tp;
 }
 
-cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
+cudaError_t launch_tree(const TreeParams& p, const TreeMma& t, const TreePlan& plan, cudaStream_t s) {
   cudaError_t e = cudaErrorInvalidValue;
+  if (plan.mma) {
+    e = launch_tree_mma(p, t, plan.grid_splits, plan.pair, s);
+    if (e != cudaSuccess || plan.parts == 1) return e;
+    return p.c.d == 128 ? launch_merge<128>(p, s) : launch_merge<64>(p, s);
+  }
 #define HEADQ_TREE_D(D)                                              \
   case D:                                                            \
     e = launch_any<D>(p, s);                                         \

@@ -1,0 +1,868 @@
+// headq_tree_attn on the tensor cores: bf16 queries, bf16 or 2-bit values, d 64 or 128,
+// r 0, 8 or 16 ("HeadQ: Model-Visible Distortion and Score-Space Correction for KV-Cache
+// Quantization", gist.science summary, section 3, step 3).
+//
+// The n * G query rows of a (sequence, KV head) fill the M side of tcgen05.mma, 128 rows a
+// block; 128-token tiles of the cache are the N side of the logits and the K side of the
+// readout.  A logit is one dot product of length d + r: q with the decoded base key, and
+// U_h^T q with the decoded side code.
+//
+// tree_prep_kernel   once per call: query rows as fp16 operands, each scaled by its own
+//   power of two (exact for bf16 queries but for elements 2^-28 below the row's largest),
+//   U_h^T q behind them, written as the shared-memory image the main kernel copies in; the
+//   mask as bits.
+// tree_mma_kernel    one CTA of 14 warps per (row blocks, split, sequence x KV head):
+//   4 decoder warps  one thread per token: packed codes from HBM (the next tile's loads in
+//     flight) to fp16 keys in shared memory, scaled by a power of two per tile.  The four
+//     levels min + code * scale of a 32-channel group are rounded to fp16 once, two 2-bit
+//     codes then pick their pair by one byte permute; the channels come out as a 4 x 4
+//     transpose within each 16, and the queries are stored in that order too.  2-bit values
+//     the same way in bf16.
+//   1 TMA warp       dense bf16 values, 64 tokens x 64 channels a box
+//   1 MMA thread     logits into TMEM, readout from the weights in TMEM
+//   2 x 4 softmax warps (two "lanes"), one thread per query row.  PAIR (more than 128 rows):
+//     the lanes hold two row blocks over the same tiles, so each decoded tile serves 256
+//     rows; else they take alternate tiles of the one block and end as two splits.
+// The running maximum is refreshed lazily (when a logit exceeds it by 2^8): one pass over
+// the logits, and the output accumulator in TMEM is rescaled only then.  Weights are
+// truncated to bf16 and the sum is taken over the truncated weights, so that the error of
+// a weight cancels where one token holds most of it; the log-sum-exp, when asked for, is
+// summed over the unrounded ones.
+//
+// TMEM (512 columns): logits of lane l at 128 l (its weights overwrite them, two to a
+// column), outputs at 256 + 128 l.
+#include <cuda_fp16.h>
+
+#include "decode_common.cuh"
+#include "tree.cuh"
+
+namespace headq {
+namespace {
+
+using dc::mbar_arrive;
+using dc::mbar_expect_tx;
+using dc::mbar_init;
+using dc::mbar_wait;
+using dc::smem_addr;
+
+constexpr int kTile = 128;          // tokens per tile
+constexpr int kBlock = 128;         // query rows per block
+constexpr int kThreads = 14 * 32;
+constexpr int kDecodeWarp = 8, kMmaWarp = 12, kTmaWarp = 13;
+constexpr int kKStages = 2;
+constexpr int kRing = 8;            // tiles whose key scales are kept (more than can be in flight)
+constexpr float kLazy = 8.0f;       // log2 units a logit may exceed the running maximum by
+constexpr uint32_t kAll = 0xffffffffu;
+
+// bytes of 128 operand rows: d channels in 64-channel blocks (128-byte rows, 128-byte
+// swizzle), then 16 side entries (two 8-entry halves, no swizzle)
+__host__ __device__ constexpr int operand_bytes(int d, int r) { return kTile * (2 * d + (r > 0 ? 32 : 0)); }
+
+// ---------------------------------------------------------------- tcgen05
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a));
+}
+__device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+}
+__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Shared-memory matrix descriptors: start address, leading and stride byte offsets (all in
+// 16-byte units), descriptor version 1, swizzle (2: 128 bytes, 0: none).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride, uint32_t swizzle) {
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
+         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (static_cast<uint64_t>(swizzle) << 61);
+}
+// Instruction descriptor of kind::f16: fp32 accumulator, operand type (0 fp16, 1 bf16),
+// B transposed (its N side contiguous), N / 8, M / 16 with M = 128.
+__host__ __device__ constexpr uint32_t mma_desc(uint32_t type, uint32_t b_trans, uint32_t n) {
+  return (1u << 4) | (type << 7) | (type << 10) | (b_trans << 16) | ((n / 8) << 17) | ((128u / 16) << 24);
+}
+
+// 2^(14 - e) and 2^(e - 14), e the binary exponent of m >= 0: m times the first lies in
+// [2^14, 2^15), inside fp16 with 28 binades of normal numbers below.  (1, 1) when m is 0 or
+// not finite; exponents below -100 are taken as -100.
+__device__ __forceinline__ float2 operand_scale(float m) {
+  const int b = static_cast<int>(__float_as_uint(m) >> 23);
+  if (m == 0.0f || b == 255) return make_float2(1.0f, 1.0f);
+  const int e = max(b - 127, -100);
+  return make_float2(__uint_as_float(static_cast<uint32_t>(141 - e) << 23),
+                     __uint_as_float(static_cast<uint32_t>(max(113 + e, 1)) << 23));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// channel at position `pos` of an operand row (a 4 x 4 transpose within each 16)
+__host__ __device__ constexpr int channel_at(int pos) { return (pos & ~15) + 4 * (pos & 3) + ((pos >> 2) & 3); }
+
+// byte offset of 16-byte chunk c of row x in the swizzled blocks of an operand
+__device__ __forceinline__ int swz(int x, int c) { return (c >> 3) * (kTile * 128) + x * 128 + (((c & 7) ^ (x & 7)) << 4); }
+
+// zeroes the bf16 values of a pair that are not finite; whether there were any
+__device__ __forceinline__ bool drop_bad(uint32_t& v) {
+  const bool lo = (v & 0x7f80u) == 0x7f80u, hi = (v & 0x7f800000u) == 0x7f800000u;
+  if (lo) v &= 0xffff0000u;
+  if (hi) v &= 0x0000ffffu;
+  return lo || hi;
+}
+
+// 16 codes of one word as 8 operand pairs, through the group's levels (two per register)
+__device__ __forceinline__ void pick16(uint32_t w, uint32_t l01, uint32_t l23, uint4& a, uint4& b) {
+  uint32_t o[8];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    // byte j: the code of channel 4 j + s; code c picks bytes 2c, 2c + 1 of the levels
+    const uint32_t sel = ((w >> (2 * s)) & 0x03030303u) * 0x22u + 0x10101010u;
+    o[2 * s] = __byte_perm(l01, l23, sel);
+    o[2 * s + 1] = __byte_perm(l01, l23, sel >> 16);
+  }
+  a = make_uint4(o[0], o[1], o[2], o[3]);
+  b = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// ---------------------------------------------------------------- prep
+// One warp per 8 query rows of a unit's row blocks: D / 4 lanes a row, 4 operand positions
+// each.  Blocks past the rows' part pack the mask.
+constexpr int kPrepRows = 8;
+
+template <int D, int R>
+__global__ void __launch_bounds__(256)
+tree_prep_kernel(const TreeParams p, const TreeMma t, int row_ctas) {
+  const int warp = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (static_cast<int>(blockIdx.x) >= row_ctas) {  // mask bits: one warp per (sequence, row)
+    const int bi = (blockIdx.x - row_ctas) * 8 + (threadIdx.x >> 5);
+    if (!t.words || bi >= p.c.B * p.span.n) return;
+    const int b = bi / p.span.n, i = bi - b * p.span.n;
+    const int n = span_seq(p.span, b).n;
+    for (int w = 0; w < t.wpr; ++w) {
+      const int j = 32 * w + lane;
+      const bool see = i < n && j < n && tree_sees(p, b, i, j);
+      const uint32_t bits = __ballot_sync(kAll, see);
+      if (lane == 0) t.words[static_cast<size_t>(bi) * t.wpr + w] = bits;
+    }
+    return;
+  }
+  constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes per row, rows at a time
+  const int per_unit = t.blocks * kBlock / kPrepRows;
+  const int unit = warp / per_unit, x0 = (warp - unit * per_unit) * kPrepRows;
+  if (unit >= p.c.B * p.c.Hkv) return;
+  const int b = unit / p.c.Hkv, kv = unit - b * p.c.Hkv;
+  const SpanSeq sq = span_seq(p.span, b);
+  const int rows = sq.n * p.G;
+  if (x0 / 32 * 32 >= rows) return;  // a 32-row group without rows is never read
+  const int ll = lane & (LPR - 1);
+  int ch[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) ch[k] = channel_at(4 * ll + k);
+  float u[4][R > 0 ? R : 1];
+  if constexpr (R > 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < R; i += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(p.U + (static_cast<size_t>(kv) * D + ch[k]) * R + i));
+        u[k][i] = v.x; u[k][i + 1] = v.y; u[k][i + 2] = v.z; u[k][i + 3] = v.w;
+      }
+  }
+  const float sign = p.sm_scale < 0.0f ? -1.0f : 1.0f;
+  for (int it = 0; it < kPrepRows / RPW; ++it) {
+    const int x = x0 + it * RPW + lane / LPR;
+    float q[4] = {0, 0, 0, 0};
+    if (x < rows) {
+      const int i = x / p.G, g = x - i * p.G;
+      const uint16_t* src = static_cast<const uint16_t*>(p.q.ptr) + (sq.row0 + i) * p.q.row_stride +
+                            (kv * p.G + g) * p.q.head_stride;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q[k] = sign * bf16_bits_to_f32(src[ch[k]]);
+    }
+    float mx = fmaxf(fmaxf(fabsf(q[0]), fabsf(q[1])), fmaxf(fabsf(q[2]), fabsf(q[3])));
+    float side = 0.0f;
+    if constexpr (R > 0) {
+      float a[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        a[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a[i] = fmaf(q[k], u[k][i], a[i]);
+      }
+      // halve the entries a lane holds with each exchange, then sum what is left
+      int m = LPR / 2;
+#pragma unroll
+      for (int h = R / 2; h >= 1; h /= 2) {
+        const bool up = (lane & m) != 0;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+          const float keep = up ? a[i + h] : a[i], give = up ? a[i] : a[i + h];
+          a[i] = keep + __shfl_xor_sync(kAll, give, m);
+        }
+        m /= 2;
+      }
+      for (; m >= 1; m /= 2) a[0] += __shfl_xor_sync(kAll, a[0], m);
+      side = a[0] * p.corr_sign;  // entry ll / (LPR / R)
+      mx = fmaxf(mx, fabsf(side));
+    }
+#pragma unroll
+    for (int m = LPR / 2; m >= 1; m /= 2) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, m));
+    const float2 s = operand_scale(mx);
+    const int xr = x & (kBlock - 1);
+    uint8_t* img = t.qimg + (static_cast<size_t>(unit) * t.blocks + x / kBlock) * operand_bytes(D, R);
+    *reinterpret_cast<uint2*>(img + swz(xr, ll / 2) + 8 * (ll & 1)) =
+        make_uint2(pack_f16(q[0] * s.x, q[1] * s.x), pack_f16(q[2] * s.x, q[3] * s.x));
+    if constexpr (R > 0) {
+      __half* zb = reinterpret_cast<__half*>(img + D / 64 * (kTile * 128));
+      const int e = ll / (LPR / R);
+      if (ll % (LPR / R) == 0) zb[(e / 8) * (kTile * 8) + xr * 8 + (e & 7)] = __float2half_rn(side * s.x);
+      if (R == 8 && ll < 8) zb[kTile * 8 + xr * 8 + ll] = __float2half_rn(0.0f);
+    }
+    if (ll == 0)
+      t.qf[static_cast<size_t>(unit) * t.blocks * kBlock + x] = s.y * (fabsf(p.sm_scale) * dc::kLog2e);
+  }
+}
+
+// ---------------------------------------------------------------- main kernel
+template <int D, int R, bool V2, bool PAIR>
+struct Layout {
+  static constexpr int kVStages = PAIR ? 2 : 3;
+  static constexpr int kOperand = operand_bytes(D, R);
+  static constexpr int kVTile = kTile * D * 2;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + (PAIR ? 2 : 1) * kOperand;
+  static constexpr int kV = kK + kKStages * kOperand;
+  static constexpr int kScale = kV + kVStages * kVTile;  // [kRing][kTile] floats
+  static constexpr int kBars = kScale + kRing * kTile * 4;
+  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 6;
+  static constexpr int kMisc = (kBars + 8 * kNumBars + 15) & ~15;  // tmem base, bad-value flag, 2 x 4 maxima
+  static constexpr int kBytes = kMisc + 64 + 1024;    // and room for the alignment
+};
+
+// What a decoder thread holds of its token.
+template <int D, int R, bool V2>
+struct RawToken {
+  static constexpr int NG = D / 32;
+  uint4 kc[D / 64];
+  float ks[NG], km[NG];
+  uint32_t zc[R > 0 ? R / 8 : 1];
+  float zs;
+  uint4 vc[V2 ? D / 64 : 1];
+  float vs[V2 ? NG : 1], vm[V2 ? NG : 1];
+};
+
+template <int NG>
+__device__ __forceinline__ void load_groups(const float* p, size_t row, float (&x)[NG]) {
+  if constexpr (NG == 4) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + row);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  } else {
+    const float2 v = __ldg(reinterpret_cast<const float2*>(p) + row);
+    x[0] = v.x; x[1] = v.y;
+  }
+}
+
+// the codes of the token at position t, all zero at and past t_hi
+template <int D, int R, bool V2>
+__device__ __forceinline__ void load_token(const TreeParams& p, int b, int kv, int t, int t_hi,
+                                           RawToken<D, R, V2>& x) {
+  constexpr int NG = D / 32;
+  if (t >= t_hi) {
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) x.kc[k] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) x.ks[g] = x.km[g] = 0.0f;
+    if constexpr (R > 0) {
+#pragma unroll
+      for (int k = 0; k < R / 8; ++k) x.zc[k] = 0u;
+    }
+    x.zs = 0.0f;
+    if constexpr (V2) {
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) x.vc[k] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) x.vs[g] = x.vm[g] = 0.0f;
+    }
+    return;
+  }
+  const size_t row = cache_row_read(p.c, b, kv, t, p.err);
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k) x.kc[k] = __ldg(reinterpret_cast<const uint4*>(p.c.k_codes + row * (D / 4)) + k);
+  load_groups<NG>(p.c.k_scale, row, x.ks);
+  load_groups<NG>(p.c.k_min, row, x.km);
+  x.zs = 0.0f;
+  if constexpr (R > 0) {
+    const uint32_t* z = reinterpret_cast<const uint32_t*>(p.c.z_codes + row * (R / 2));
+#pragma unroll
+    for (int k = 0; k < R / 8; ++k) x.zc[k] = __ldg(z + k);
+    x.zs = __ldg(p.c.z_scale + row);
+  }
+  if constexpr (V2) {
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) x.vc[k] = __ldg(reinterpret_cast<const uint4*>(p.c.v_codes + row * (D / 4)) + k);
+    load_groups<NG>(p.c.v_scale, row, x.vs);
+    load_groups<NG>(p.c.v_min, row, x.vm);
+  }
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& a, int k) {
+  return k == 0 ? a.x : k == 1 ? a.y : k == 2 ? a.z : a.w;
+}
+
+// 32 mask bits of new token i's row from bit a (new-token index of the first; bits below 0
+// are the prefix: seen)
+__device__ __forceinline__ uint32_t mask_word(const uint32_t* row, int wpr, int i, int k) {
+  if (k < 0) return kAll;
+  if (row) return k < wpr ? __ldg(row + k) : 0u;
+  const int last = i - 32 * k;  // j <= i
+  return last < 0 ? 0u : last >= 31 ? kAll : (2u << last) - 1u;
+}
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int wpr, int i, int a) {
+  const int k = a >> 5;
+  return __funnelshift_r(mask_word(row, wpr, i, k), mask_word(row, wpr, i, k + 1), a & 31);
+}
+
+template <int D, int R, bool V2, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUtensorMap vmap) {
+  using Ly = Layout<D, R, V2, PAIR>;
+  constexpr int NG = D / 32;
+  constexpr int VS = Ly::kVStages;
+  extern __shared__ uint8_t raw_smem[];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int unit = blockIdx.z, b = unit / p.c.Hkv, kv = unit - b * p.c.Hkv;
+  const SpanSeq sq = span_seq(p.span, b);
+  const int rows = sq.n * p.G, xb = blockIdx.x * (PAIR ? 2 : 1) * kBlock;
+  if (xb >= rows) return;
+  const int P = sq.p0, L = sq.p0 < 0 ? 0 : sq.p0 + sq.n;
+  const int t_lo = blockIdx.y * p.chunk, t_hi = min(L, t_lo + p.chunk);
+  const int tiles = t_hi > t_lo ? (t_hi - t_lo + kTile - 1) / kTile : 0;
+  const int lane_parts = p.splits / gridDim.y;  // 2 when the lanes end as two splits
+  const size_t part_rows = static_cast<size_t>(p.span.n) * p.G;
+  // this softmax thread's query row
+  const int wl = (warp >> 2) & 1;  // lane of the softmax warp
+  const int x = xb + (PAIR ? wl * kBlock : 0) + (warp & 3) * 32 + lane;
+
+  if (tiles == 0) {  // nothing to read: the rows' share of this split is empty
+    if (warp < 8 && x < rows && (PAIR || wl < lane_parts)) {
+      if (p.splits > 1) {
+        p.part_ml[(static_cast<size_t>(unit) * p.splits + blockIdx.y * lane_parts + (PAIR ? 0 : wl)) * part_rows + x] =
+            make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+      } else {
+        const int i = x / p.G, h = kv * p.G + x - i * p.G;
+        const size_t orow = static_cast<size_t>(sq.row0) + i;
+        for (int c = 0; c < D; c += 4)
+          store_row4(p.out, orow * p.out.row_stride + h * p.out.head_stride + c, make_float4(0, 0, 0, 0));
+        if (p.lse) p.lse[orow * p.Hq + h] = -INFINITY;
+      }
+    }
+    return;
+  }
+
+  uint8_t* sm = smem_align(raw_smem, 1024);
+  const uint32_t base = smem_addr(sm);
+  float* scale_s = reinterpret_cast<float*>(sm + Ly::kScale);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(sm + Ly::kMisc);
+  const uint32_t bars = base + Ly::kBars;
+  const uint32_t q_full = bars;
+  auto k_full = [&](int s) { return bars + 8 * (1 + s); };
+  auto k_empty = [&](int s) { return bars + 8 * (1 + kKStages + s); };
+  auto v_full = [&](int s) { return bars + 8 * (1 + 2 * kKStages + s); };
+  auto v_empty = [&](int s) { return bars + 8 * (1 + 2 * kKStages + VS + s); };
+  auto s_full = [&](int l) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + l); };
+  auto p_full = [&](int l) { return bars + 8 * (3 + 2 * kKStages + 2 * VS + l); };
+  auto o_done = [&](int l) { return bars + 8 * (5 + 2 * kKStages + 2 * VS + l); };
+
+  // tiles of lane l: PAIR all of them (when the lane has rows), else those of its parity
+  const int lanes_on = PAIR ? (xb + kBlock < rows ? 2 : 1) : (tiles > 1 ? 2 : 1);
+  auto lane_tiles = [&](int l) { return l >= lanes_on ? 0 : PAIR ? tiles : (tiles - l + 1) / 2; };
+  auto tile_of = [&](int l, int k) { return PAIR ? k : 2 * k + l; };
+
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(k_full(s), 4);
+      mbar_init(k_empty(s), PAIR ? lanes_on : 1);
+    }
+    for (int s = 0; s < VS; ++s) {
+      mbar_init(v_full(s), V2 ? 4 : 1);
+      mbar_init(v_empty(s), PAIR ? lanes_on : 1);
+    }
+    for (int l = 0; l < 2; ++l) {
+      const int r0 = rows - xb - (PAIR ? l * kBlock : 0);
+      mbar_init(s_full(l), 1);
+      mbar_init(p_full(l), max(1, min(4, (r0 + 31) / 32)));  // warps that have rows
+      mbar_init(o_done(l), 1);
+    }
+    misc[1] = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_smem();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(misc)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
+  bool ok = true;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      const int nq = PAIR ? lanes_on : 1;
+      mbar_expect_tx(q_full, nq * Ly::kOperand);
+      const uint8_t* img = t.qimg + (static_cast<size_t>(unit) * t.blocks + xb / kBlock) * Ly::kOperand;
+      dc::bulk_g2s(base + Ly::kQ, img, nq * Ly::kOperand, q_full);
+      if constexpr (!V2) {
+        int issued = 0;
+        for (int k = 0; k < tiles && ok; ++k) {
+          const int s = k % VS;
+          if (k >= VS && !mbar_wait(v_empty(s), ((k / VS) - 1) & 1)) { ok = false; break; }
+          const int t0 = t_lo + k * kTile;
+          const int halves = t0 + 64 < t_hi ? 2 : 1;
+          mbar_expect_tx(v_full(s), halves * 64 * D * 2);
+          for (int h = 0; h < halves; ++h) {
+            const CacheSlab sl = cache_slab_read(p.c, b, kv, t0 + 64 * h, p.err);
+            for (int c = 0; c < D / 64; ++c)
+              dc::tma_3d(base + Ly::kV + s * Ly::kVTile + c * (kTile * 128) + h * (64 * 128), &vmap, 64 * c, sl.off,
+                         static_cast<int>(sl.slab), v_full(s));
+          }
+          issued = k + 1;
+        }
+        // no copy is in flight when the CTA ends
+        for (int k = max(0, issued - VS); k < issued; ++k) mbar_wait(v_full(k % VS), (k / VS) & 1);
+      }
+      if (!mbar_wait(q_full, 0)) ok = false;
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      constexpr uint32_t kLogit = mma_desc(0, 0, kTile);       // fp16, both operands K-major
+      constexpr uint32_t kRead = mma_desc(1, 1, D);            // bf16, values channel-major
+      ok = mbar_wait(q_full, 0);
+      int k[2] = {0, 0};
+      bool have_s[2] = {false, false};
+      long long start = clock64();
+      while (ok && (k[0] < lane_tiles(0) || k[1] < lane_tiles(1))) {
+        bool moved = false;
+#pragma unroll
+        for (int l = 0; l < 2; ++l) {
+          if (k[l] >= lane_tiles(l)) continue;
+          const int tile = tile_of(l, k[l]);
+          if (!have_s[l]) {  // logits of the lane's next tile, once its last readout is done
+            const int s = tile % kKStages;
+            if (k[l] > 0 && !mbar_test(o_done(l), (k[l] - 1) & 1)) continue;
+            if (!mbar_test(k_full(s), (tile / kKStages) & 1)) continue;
+            tc_fence_after();
+            const uint32_t qa = base + Ly::kQ + (PAIR ? l * Ly::kOperand : 0), ka = base + Ly::kK + s * Ly::kOperand;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                tc_mma_ss(tmem + 128 * l, smem_desc(qa + c * (kTile * 128) + 32 * e, 16, 1024, 2),
+                          smem_desc(ka + c * (kTile * 128) + 32 * e, 16, 1024, 2), kLogit, c + e > 0);
+            if constexpr (R > 0)
+              tc_mma_ss(tmem + 128 * l, smem_desc(qa + D / 64 * (kTile * 128), kTile * 16, 128, 0),
+                        smem_desc(ka + D / 64 * (kTile * 128), kTile * 16, 128, 0), kLogit, true);
+            tc_commit(s_full(l));
+            tc_commit(k_empty(s));
+            have_s[l] = true;
+            moved = true;
+          } else {  // readout of the lane's tile
+            const int s = tile % VS;
+            if (!mbar_test(p_full(l), k[l] & 1) || !mbar_test(v_full(s), (tile / VS) & 1)) continue;
+            tc_fence_after();
+            const uint32_t va = base + Ly::kV + s * Ly::kVTile;
+#pragma unroll
+            for (int e = 0; e < kTile / 16; ++e)
+              tc_mma_ts(tmem + 256 + 128 * l, tmem + 128 * l + 8 * e, smem_desc(va + 2048 * e, kTile * 128, 1024, 2),
+                        kRead, k[l] > 0 || e > 0);
+            tc_commit(o_done(l));
+            tc_commit(v_empty(s));
+            have_s[l] = false;
+            ++k[l];
+            moved = true;
+          }
+        }
+        if (moved) start = clock64();
+        else if (clock64() - start > dc::kWaitCycles) ok = false;
+      }
+      // the products are done before TMEM is given back
+      for (int l = 0; l < 2; ++l)
+        if (k[l] > 0 && !mbar_wait(o_done(l), (k[l] - 1) & 1)) ok = false;
+    }
+  } else if (warp >= kDecodeWarp) {
+    const int tok = tid - kDecodeWarp * 32;
+    float* red = reinterpret_cast<float*>(misc + 4);  // [2][4] warp maxima
+    RawToken<D, R, V2> cur, nxt;
+    load_token<D, R, V2>(p, b, kv, t_lo + tok, t_hi, cur);
+    for (int k = 0; k < tiles; ++k) {
+      const int t0 = t_lo + k * kTile, s = k % kKStages, sv = k % VS;
+      if (k + 1 < tiles) load_token<D, R, V2>(p, b, kv, t0 + kTile + tok, t_hi, nxt);
+      const bool tail = t0 + kTile > min(P, t_hi);  // holds new tokens, or ends the sequence
+      float mx = 7.0f * fabsf(cur.zs);
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+        mx = fmaxf(mx, fmaxf(fabsf(cur.km[g]), fabsf(fmaf(3.0f, cur.ks[g], cur.km[g]))));
+      if (!tail) {  // one power of two per tile
+        const uint32_t w = __reduce_max_sync(kAll, __float_as_uint(mx));
+        if (lane == 0) red[(k & 1) * 4 + warp - kDecodeWarp] = __uint_as_float(w);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const float4 m4 = *reinterpret_cast<const float4*>(red + (k & 1) * 4);
+        mx = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+      } else {  // one per token: an unseen new token's size touches no other
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      }
+      const float2 sc = operand_scale(mx);
+      if (k >= kKStages && ok && !mbar_wait(k_empty(s), ((k / kKStages) - 1) & 1)) ok = false;
+      scale_s[(k % kRing) * kTile + tok] = sc.y;
+      uint8_t* ks = sm + Ly::kK + s * Ly::kOperand;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const float m = cur.km[g], d = cur.ks[g];
+        const uint32_t l01 = pack_f16(m * sc.x, fmaf(1.0f, d, m) * sc.x);
+        const uint32_t l23 = pack_f16(fmaf(2.0f, d, m) * sc.x, fmaf(3.0f, d, m) * sc.x);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4 a, c;
+          pick16(word_of(cur.kc[g / 2], 2 * (g & 1) + h), l01, l23, a, c);
+          *reinterpret_cast<uint4*>(ks + swz(tok, 4 * g + 2 * h)) = a;
+          *reinterpret_cast<uint4*>(ks + swz(tok, 4 * g + 2 * h + 1)) = c;
+        }
+      }
+      if constexpr (R > 0) {
+        const float zs = cur.zs * sc.x;
+        uint4* zb = reinterpret_cast<uint4*>(ks + D / 64 * (kTile * 128));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t o[4] = {0, 0, 0, 0};
+          if (h < R / 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // nibble ^ 8 is w + 8; 2^23 + that has it in its low mantissa bits
+              const uint32_t w = cur.zc[h < R / 8 ? h : 0] >> (8 * e);
+              const float a = __uint_as_float(0x4B000000u | ((w & 15u) ^ 8u)) - 8388616.0f;
+              const float c = __uint_as_float(0x4B000000u | (((w >> 4) & 15u) ^ 8u)) - 8388616.0f;
+              o[e] = pack_f16(a * zs, c * zs);
+            }
+          }
+          zb[h * kTile + tok] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      if constexpr (V2) {
+        if (k >= VS && ok && !mbar_wait(v_empty(sv), ((k / VS) - 1) & 1)) ok = false;
+        uint8_t* vs = sm + Ly::kV + sv * Ly::kVTile;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float m = cur.vm[g], d = cur.vs[g];
+          uint32_t l01 = pack_bf16(m, fmaf(1.0f, d, m)), l23 = pack_bf16(fmaf(2.0f, d, m), fmaf(3.0f, d, m));
+          // a new token's value that is not finite must not meet the zero weights of the
+          // rows that do not see it: it is left out here and added to the rows that do
+          if (t0 + tok >= P && (drop_bad(l01) | drop_bad(l23))) misc[1] = 1u;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint4 a, c;
+            pick16(word_of(cur.vc[g / 2], 2 * (g & 1) + h), l01, l23, a, c);
+            *reinterpret_cast<uint4*>(vs + swz(tok, 4 * g + 2 * h)) = a;
+            *reinterpret_cast<uint4*>(vs + swz(tok, 4 * g + 2 * h + 1)) = c;
+          }
+        }
+      } else if (tail) {
+        // the last rows of the value tile: nothing past the end, and as above for new tokens
+        if (ok && !mbar_wait(v_full(sv), (k / VS) & 1)) ok = false;
+        uint8_t* vs = sm + Ly::kV + sv * Ly::kVTile;
+        if (t0 + tok >= P) {
+          const bool past = t0 + tok >= t_hi;
+          for (int c = 0; c < D / 8; ++c) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(vs + swz(tok, c));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t v = past ? 0u : w[e];
+              if (drop_bad(v)) misc[1] = 1u;
+              w[e] = v;
+            }
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(k_full(s));
+        if (V2) mbar_arrive(v_full(sv));
+      }
+      cur = nxt;
+    }
+  } else if (xb + (PAIR ? wl * kBlock : 0) + (warp & 3) * 32 < rows && wl < lanes_on) {
+    // ---- softmax and epilogue of this warp's 32 query rows
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + 128 * wl + lane_off, to = tmem + 256 + 128 * wl + lane_off;
+    const int i = min(x, rows - 1) / p.G;
+    const float fq = t.qf[static_cast<size_t>(unit) * t.blocks * kBlock + x];
+    const uint32_t* words = t.words ? t.words + (static_cast<size_t>(b) * p.span.n + i) * t.wpr : nullptr;
+    const bool want_lse = p.lse != nullptr;
+    float m = -INFINITY, l = 0.0f, lx = 0.0f;
+    const int nk = lane_tiles(wl);
+    for (int k = 0; k < nk; ++k) {
+      const int tile = tile_of(wl, k), t0 = t_lo + tile * kTile;
+      if (!mbar_wait(s_full(wl), k & 1)) { ok = false; break; }
+      tc_fence_after();
+      const float* col = scale_s + (tile % kRing) * kTile;
+      const bool tail = t0 + kTile > min(P, t_hi);
+      const float f = fmaxf(tail ? fq : fq * col[0], 1e-37f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t sr[32];
+        tc_ld32(ts + 32 * c, sr);
+        tc_wait_ld();
+        float s[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(sr[j]);
+        if (tail) {
+          const uint32_t bits = mask_bits(words, t.wpr, i, t0 + 32 * c - P);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[j] = (bits >> j) & 1u ? s[j] * col[32 * c + j] : -INFINITY;
+        }
+        float mx = s[0];
+#pragma unroll
+        for (int j = 1; j < 32; ++j) mx = fmaxf(mx, s[j]);
+        const float top = mx * f;
+        const bool raise = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
+        if (__any_sync(kAll, raise)) {
+          const float m2 = raise ? top : m;
+          const float a = m == -INFINITY ? 0.0f : ex2(m - m2);
+          l *= a;
+          lx *= a;
+          m = m2;
+          if (k > 0) {
+#pragma unroll
+            for (int o = 0; o < D; o += 16) {
+              uint32_t w[16];
+              tc_ld16(to + o, w);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * a);
+              tc_st16(to + o, w);
+            }
+          }
+          for (int o = 0; o < c; ++o) {  // this tile's weights so far
+            uint32_t w[16];
+            tc_ld16(ts + 16 * o, w);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float e0 = __uint_as_float(w[j] << 16) * a, e1 = __uint_as_float(w[j] & 0xffff0000u) * a;
+              const uint32_t h0 = __float_as_uint(e0) & 0xffff0000u, h1 = __float_as_uint(e1) & 0xffff0000u;
+              l += (__uint_as_float(h0) - e0) + (__uint_as_float(h1) - e1);
+              w[j] = (h0 >> 16) | h1;
+            }
+            tc_st16(ts + 16 * o, w);
+          }
+          tc_wait_st();
+        }
+        const float mm = m == -INFINITY ? 0.0f : m;
+        const uint64_t f2 = codec::pk2(f, f), m2 = codec::pk2(-mm, -mm);
+        uint32_t w[16];
+        uint64_t sum = 0ull, sumx = 0ull;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint64_t y = codec::fma2(codec::pk2(s[2 * j], s[2 * j + 1]), f2, m2);
+          const float e0 = ex2(codec::pk_lo(y)), e1 = ex2(codec::pk_hi(y));
+          const uint32_t h0 = __float_as_uint(e0) & 0xffff0000u, h1 = __float_as_uint(e1) & 0xffff0000u;
+          w[j] = __byte_perm(h0, h1, 0x7632);
+          sum = codec::add2(sum, codec::pk2(__uint_as_float(h0), __uint_as_float(h1)));
+          if (want_lse) sumx = codec::add2(sumx, codec::pk2(e0, e1));
+        }
+        l += codec::pk_lo(sum) + codec::pk_hi(sum);
+        lx += codec::pk_lo(sumx) + codec::pk_hi(sumx);
+        tc_st16(ts + 16 * c, w);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(wl));
+    }
+    if (ok && nk > 0 && !mbar_wait(o_done(wl), (nk - 1) & 1)) ok = false;
+    tc_fence_after();
+    if (ok) {
+      const bool bad = *reinterpret_cast<volatile uint32_t*>(misc + 1) != 0u;
+      const bool direct = p.splits == 1;
+      const int part = blockIdx.y * lane_parts + (PAIR ? 0 : wl);
+      const size_t pr = (static_cast<size_t>(unit) * p.splits + part) * part_rows + x;
+      const int h = kv * p.G + x - i * p.G;
+      const size_t orow = static_cast<size_t>(sq.row0) + i;
+      const float inv = !direct ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t w[32];
+        tc_ld32(to + 32 * c, w);
+        tc_wait_ld();
+        float o[32];  // in channel order
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[V2 ? channel_at(j) : j] = __uint_as_float(w[j]);
+        if (l == 0.0f) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+        }
+        if (bad && x < rows) {  // values that are not finite, for the rows that see them
+          for (int tt = max(P, t_lo); tt < t_hi; ++tt) {
+            const int tl = (tt - t_lo) / kTile;
+            if (!PAIR && (tl & 1) != wl) continue;
+            if (!((mask_word(words, t.wpr, i, (tt - P) >> 5) >> ((tt - P) & 31)) & 1u)) continue;
+            const size_t row = cache_row_read(p.c, b, kv, tt, p.err);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int ch = 32 * c + j;
+              const float v = V2 ? fmaf(static_cast<float>(code2(p.c.v_codes + row * (D / 4), ch)),
+                                        p.c.v_scale[row * NG + c], p.c.v_min[row * NG + c])
+                                 : load_elem(p.c.v, row * D + ch, true);
+              if (!(fabsf(v) < 0x1.FFp127f)) o[j] += v;  // not finite once rounded to bf16
+            }
+          }
+        }
+        if (x < rows) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 v = make_float4(o[j] * inv, o[j + 1] * inv, o[j + 2] * inv, o[j + 3] * inv);
+            if (direct) store_row4(p.out, orow * p.out.row_stride + h * p.out.head_stride + 32 * c + j, v);
+            else *reinterpret_cast<float4*>(p.part_o + pr * D + 32 * c + j) = v;
+          }
+        }
+      }
+      if (x < rows) {
+        if (!direct) p.part_ml[pr] = make_float4(m * dc::kLn2, l, lx, 0.0f);
+        else if (want_lse) p.lse[orow * p.Hq + h] = l == 0.0f ? -INFINITY : m * dc::kLn2 + logf(lx);
+      }
+    }
+  } else if (warp < 8 && x < rows && !PAIR && wl < lane_parts) {
+    // the lane without a tile: its split is empty
+    p.part_ml[(static_cast<size_t>(unit) * p.splits + blockIdx.y * lane_parts + wl) * part_rows + x] =
+        make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+  }
+
+  if (!ok) atomicOr(p.err, kDevErrWaitTimeout);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  __syncwarp();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+template <int D, int R, bool V2, bool PAIR>
+cudaError_t launch_main(const TreeParams& p, const TreeMma& t, int grid_splits, cudaStream_t s) {
+  CUtensorMap map{};
+  if (!V2) {
+    const uint64_t slabs = p.c.page_size ? static_cast<uint64_t>(p.c.num_pages) * p.c.Hkv
+                                         : static_cast<uint64_t>(p.c.B) * p.c.Hkv;
+    const uint64_t rows = p.c.page_size ? p.c.page_size : p.c.T_cap;
+    if (!encode_bf16_rows(&map, p.c.v, D, rows, slabs, 64)) return cudaErrorInvalidValue;
+  }
+  auto k = tree_mma_kernel<D, R, V2, PAIR>;
+  constexpr int smem = Layout<D, R, V2, PAIR>::kBytes;
+  static_assert(smem <= 232448, "shared memory of one CTA");
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  dim3 grid((t.blocks + (PAIR ? 1 : 0)) / (PAIR ? 2 : 1), grid_splits, p.c.B * p.c.Hkv);
+  k<<<grid, kThreads, smem, s>>>(p, t, map);
+  return cudaGetLastError();
+}
+
+template <int D, int R>
+cudaError_t launch_dr(const TreeParams& p, const TreeMma& t, int grid_splits, bool pair, cudaStream_t s) {
+  const long long warps = static_cast<long long>(p.c.B) * p.c.Hkv * t.blocks * (kBlock / kPrepRows);
+  const int row_ctas = static_cast<int>((warps + 7) / 8);
+  const int mask_ctas = t.words ? (p.c.B * p.span.n + 7) / 8 : 0;
+  tree_prep_kernel<D, R><<<row_ctas + mask_ctas, 256, 0, s>>>(p, t, row_ctas);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (p.c.vmode == HEADQ_V_2BIT)
+    return pair ? launch_main<D, R, true, true>(p, t, grid_splits, s)
+                : launch_main<D, R, true, false>(p, t, grid_splits, s);
+  return pair ? launch_main<D, R, false, true>(p, t, grid_splits, s)
+              : launch_main<D, R, false, false>(p, t, grid_splits, s);
+}
+
+}  // namespace
+
+bool tree_mma_supported(const headq_cache& c) {
+  return (c.d == 64 || c.d == 128) && (c.r == 0 || c.r == 8 || c.r == 16) && c.kmode == HEADQ_K_TOKEN &&
+         (c.vmode == HEADQ_V_2BIT || c.v_dtype == HEADQ_BF16) && tensor_maps_available();
+}
+
+size_t tree_mma_image_bytes(const headq_cache& c) { return operand_bytes(c.d, c.r); }
+
+cudaError_t launch_tree_mma(const TreeParams& p, const TreeMma& t, int grid_splits, bool pair, cudaStream_t s) {
+  if (p.c.d == 128) {
+    if (p.c.r == 16) return launch_dr<128, 16>(p, t, grid_splits, pair, s);
+    if (p.c.r == 8) return launch_dr<128, 8>(p, t, grid_splits, pair, s);
+    return launch_dr<128, 0>(p, t, grid_splits, pair, s);
+  }
+  if (p.c.r == 16) return launch_dr<64, 16>(p, t, grid_splits, pair, s);
+  if (p.c.r == 8) return launch_dr<64, 8>(p, t, grid_splits, pair, s);
+  return launch_dr<64, 0>(p, t, grid_splits, pair, s);
+}
+
+}  // namespace headq
