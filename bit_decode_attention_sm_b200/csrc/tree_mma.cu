@@ -11,20 +11,21 @@
 //   power of two (exact for bf16 queries but for elements 2^-28 below the row's largest),
 //   U_h^T q behind them, written as the shared-memory image the main kernel copies in; the
 //   mask as bits.
-// tree_mma_kernel    one CTA of 14 warps per (row blocks, split, sequence x KV head):
-//   4 decoder warps  one thread per token: packed codes from HBM (the next tile's loads in
+// tree_mma_kernel    one CTA of 20 warps per (row blocks, split, sequence x KV head):
+//   8 decoder warps  two threads per token, half the channels each: packed codes from HBM (the next tile's loads in
 //     flight) to fp16 keys in shared memory, scaled by a power of two per tile.  The four
 //     levels min + code * scale of a 32-channel group are rounded to fp16 once, two 2-bit
 //     codes then pick their pair by one byte permute; the channels come out as a 4 x 4
 //     transpose within each 16, and the queries are stored in that order too.  2-bit values
 //     the same way in bf16.
 //   1 TMA warp       dense bf16 values, 64 tokens x 64 channels a box
-//   1 MMA thread     logits into TMEM, readout from the weights in TMEM
+//   2 MMA warps      one per lane (below): logits into TMEM, readout from the weights there
 //   2 x 4 softmax warps (two "lanes"), one thread per query row.  PAIR (more than 128 rows):
 //     the lanes hold two row blocks over the same tiles, so each decoded tile serves 256
 //     rows; else they take alternate tiles of the one block and end as two splits.
-// The running maximum is refreshed lazily (when a logit exceeds it by 2^8): one pass over
-// the logits, and the output accumulator in TMEM is rescaled only then.  Weights are
+// The running maximum is refreshed lazily (when a logit exceeds it by 2^40): one pass over
+// the logits, and the output accumulator in TMEM is rescaled only then, which peaked
+// attention would do for some row of a warp in a third of the 32-token steps at 2^8.  Weights are
 // truncated to bf16 and the sum is taken over the truncated weights, so that the error of
 // a weight cancels where one token holds most of it; the log-sum-exp, when asked for, is
 // summed over the unrounded ones.
@@ -42,16 +43,21 @@ namespace {
 using dc::mbar_arrive;
 using dc::mbar_expect_tx;
 using dc::mbar_init;
-using dc::mbar_wait;
 using dc::smem_addr;
 
 constexpr int kTile = 128;          // tokens per tile
 constexpr int kBlock = 128;         // query rows per block
-constexpr int kThreads = 14 * 32;
-constexpr int kDecodeWarp = 8, kMmaWarp = 12, kTmaWarp = 13;
+constexpr int kThreads = 20 * 32;  // five whole warpgroups
+// registers per thread after the split: 8 x 32 x 128 + 8 x 32 x 80 + 4 x 32 x 48 = 59392, of
+// the 640 x 96 = 61440 that the block holds at launch
+constexpr int kRegsSoftmax = 128, kRegsDecode = 80, kRegsOther = 48;
+constexpr int kDecodeWarp = 8, kMmaWarp = 16, kTmaWarp = 18;  // one MMA warp per lane
 constexpr int kKStages = 2;
 constexpr int kRing = 8;            // tiles whose key scales are kept (more than can be in flight)
-constexpr float kLazy = 8.0f;       // log2 units a logit may exceed the running maximum by
+// log2 units by which a logit may exceed the running maximum before that is raised.  Weights,
+// sums and accumulators all have the 8-bit exponent of fp32, so a weight of 2^40 costs no
+// precision; sums stay finite for values below 2^70.
+constexpr float kLazy = 40.0f;
 constexpr uint32_t kAll = 0xffffffffu;
 
 // bytes of 128 operand rows: d channels in 64-channel blocks (128-byte rows, 128-byte
@@ -61,21 +67,33 @@ __host__ __device__ constexpr int operand_bytes(int d, int r) { return kTile * (
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// The next three are executed by the whole warp and take effect for the thread with `one`
+// set: their operands are then the same in every lane, and need no moves out of per-thread
+// registers between one product and the next.
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+// descriptors as their two words
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
+                                          uint32_t idesc, bool acc, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      "{\n .reg .pred p, q;\n .reg .b64 da, db;\n setp.ne.u32 p, %6, 0;\n setp.ne.u32 q, %7, 0;\n"
+      " mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, bool acc,
+                                          uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 db;\n setp.ne.u32 p, %5, 0;\n setp.ne.u32 q, %6, 0;\n"
+      " mov.b64 db, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(one)
       : "memory");
 }
 __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
@@ -89,13 +107,15 @@ __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(a));
 }
-__device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(a));
+__device__ __forceinline__ void tc_ld4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+__device__ __forceinline__ void tc_st4(uint32_t a, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0,%1,%2,%3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(a)
+               : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16]) {
   asm volatile(
@@ -107,23 +127,27 @@ __device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
+// Wait for the phase of the given parity; false after about 2 s (every try suspends the warp
+// for a while by itself).  Short: it is in many places, and five roles share the SM's
+// instruction cache.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  if (dc::mbar_try_wait(bar, parity)) return true;
+  const long long start = clock64();
+#pragma unroll 1
+  while (!dc::mbar_try_wait(bar, parity))
+    if (clock64() - start > dc::kWaitCycles) return false;
+  return true;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Shared-memory matrix descriptors: start address, leading and stride byte offsets (all in
-// 16-byte units), descriptor version 1, swizzle (2: 128 bytes, 0: none).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride, uint32_t swizzle) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
-         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (static_cast<uint64_t>(swizzle) << 61);
+// Shared-memory matrix descriptors: low word, start address and leading byte offset; high
+// word, stride byte offset, descriptor version 1 and swizzle (2: 128 bytes, 0: none); all
+// offsets in 16-byte units.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+  return ((addr & 0x3ffffu) >> 4) | ((lead >> 4) << 16);
+}
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t stride, uint32_t swizzle) {
+  return (stride >> 4) | (1u << 14) | (swizzle << 29);
 }
 // Instruction descriptor of kind::f16: fp32 accumulator, operand type (0 fp16, 1 bf16),
 // B transposed (its N side contiguous), N / 8, M / 16 with M = 128.
@@ -156,6 +180,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // channel at position `pos` of an operand row (a 4 x 4 transpose within each 16)
@@ -296,80 +326,89 @@ struct Layout {
   static constexpr int kV = kK + kKStages * kOperand;
   static constexpr int kScale = kV + kVStages * kVTile;  // [kRing][kTile] floats
   static constexpr int kBars = kScale + kRing * kTile * 4;
-  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 6;
-  static constexpr int kMisc = (kBars + 8 * kNumBars + 15) & ~15;  // tmem base, bad-value flag, 2 x 4 maxima
-  static constexpr int kBytes = kMisc + 64 + 1024;    // and room for the alignment
+  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 12;
+  static constexpr int kMisc = (kBars + 8 * kNumBars + 15) & ~15;  // tmem base, bad-value flag, 2 x 8 maxima
+  static constexpr int kBytes = kMisc + 128 + 1024;    // and room for the alignment
 };
 
-// What a decoder thread holds of its token.
+// What a decoder thread holds of its token: the codes of half the channels, all scales and
+// minima of the key (both threads of a token take their power of two from them).
 template <int D, int R, bool V2>
 struct RawToken {
-  static constexpr int NG = D / 32;
-  uint4 kc[D / 64];
+  static constexpr int NG = D / 32, W = D / 32;  // groups, code words of half the channels
+  uint32_t kw[W];
   float ks[NG], km[NG];
-  uint32_t zc[R > 0 ? R / 8 : 1];
+  uint32_t zc;
   float zs;
-  uint4 vc[V2 ? D / 64 : 1];
-  float vs[V2 ? NG : 1], vm[V2 ? NG : 1];
+  uint32_t vw[V2 ? W : 1];
+  float vs[V2 ? NG / 2 : 1], vm[V2 ? NG / 2 : 1];
 };
 
-template <int NG>
-__device__ __forceinline__ void load_groups(const float* p, size_t row, float (&x)[NG]) {
-  if constexpr (NG == 4) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + row);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-  } else {
-    const float2 v = __ldg(reinterpret_cast<const float2*>(p) + row);
-    x[0] = v.x; x[1] = v.y;
-  }
+// Loads that stay where they are written: a tile ahead of their use.
+template <int N>
+__device__ __forceinline__ void load_32(const void* p, uint32_t (&x)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "l"(p));
+  else if constexpr (N == 2)
+    asm volatile("ld.global.nc.v2.b32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "l"(p));
+  else
+    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x[0]) : "l"(p));
+}
+template <int N>
+__device__ __forceinline__ void load_f32(const float* p, float (&x)[N]) {
+  uint32_t u[N];
+  load_32<N>(p, u);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = __uint_as_float(u[i]);
 }
 
-// the codes of the token at position t, all zero at and past t_hi
+// half `h` of the token in plane row `row`
 template <int D, int R, bool V2>
-__device__ __forceinline__ void load_token(const TreeParams& p, int b, int kv, int t, int t_hi,
-                                           RawToken<D, R, V2>& x) {
-  constexpr int NG = D / 32;
-  if (t >= t_hi) {
-#pragma unroll
-    for (int k = 0; k < D / 64; ++k) x.kc[k] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) x.ks[g] = x.km[g] = 0.0f;
-    if constexpr (R > 0) {
-#pragma unroll
-      for (int k = 0; k < R / 8; ++k) x.zc[k] = 0u;
-    }
-    x.zs = 0.0f;
-    if constexpr (V2) {
-#pragma unroll
-      for (int k = 0; k < D / 64; ++k) x.vc[k] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) x.vs[g] = x.vm[g] = 0.0f;
-    }
-    return;
-  }
-  const size_t row = cache_row_read(p.c, b, kv, t, p.err);
-#pragma unroll
-  for (int k = 0; k < D / 64; ++k) x.kc[k] = __ldg(reinterpret_cast<const uint4*>(p.c.k_codes + row * (D / 4)) + k);
-  load_groups<NG>(p.c.k_scale, row, x.ks);
-  load_groups<NG>(p.c.k_min, row, x.km);
-  x.zs = 0.0f;
+__device__ __forceinline__ void load_token(const headq_cache& c, long long row, int h, RawToken<D, R, V2>& x) {
+  constexpr int NG = D / 32, W = D / 32;
+  load_32<W>(c.k_codes + row * (D / 4) + h * (D / 8), x.kw);
+  load_f32<NG>(c.k_scale + row * NG, x.ks);
+  load_f32<NG>(c.k_min + row * NG, x.km);
   if constexpr (R > 0) {
-    const uint32_t* z = reinterpret_cast<const uint32_t*>(p.c.z_codes + row * (R / 2));
-#pragma unroll
-    for (int k = 0; k < R / 8; ++k) x.zc[k] = __ldg(z + k);
-    x.zs = __ldg(p.c.z_scale + row);
+    uint32_t z[1];
+    load_32<1>(c.z_codes + row * (R / 2) + (R == 16 ? 4 * h : 0), z);
+    x.zc = z[0];
+    float f[1];
+    load_f32<1>(c.z_scale + row, f);
+    x.zs = f[0];
+  } else {
+    x.zs = 0.0f;
   }
   if constexpr (V2) {
-#pragma unroll
-    for (int k = 0; k < D / 64; ++k) x.vc[k] = __ldg(reinterpret_cast<const uint4*>(p.c.v_codes + row * (D / 4)) + k);
-    load_groups<NG>(p.c.v_scale, row, x.vs);
-    load_groups<NG>(p.c.v_min, row, x.vm);
+    load_32<W>(c.v_codes + row * (D / 4) + h * (D / 8), x.vw);
+    load_f32<NG / 2>(c.v_scale + row * NG + h * (NG / 2), x.vs);
+    load_f32<NG / 2>(c.v_min + row * NG + h * (NG / 2), x.vm);
   }
 }
 
-__device__ __forceinline__ uint32_t word_of(const uint4& a, int k) {
-  return k == 0 ? a.x : k == 1 ? a.y : k == 2 ? a.z : a.w;
-}
+// The plane rows of a decoder thread's tokens, kTile apart; past the end, the last token's.
+struct TokenRows {
+  const headq_cache& c;
+  const int32_t* table;
+  long long base;  // contiguous planes: the (sequence, KV head)'s first row
+  int kv, t, last;
+  unsigned* err;
+  __device__ TokenRows(const headq_cache& c_, int b, int kv_, int t_, int t_hi, unsigned* e)
+      : c(c_), table(c_.block_table + static_cast<size_t>(b) * c_.max_pages),
+        base((static_cast<long long>(b) * c_.Hkv + kv_) * c_.T_cap), kv(kv_), t(t_), last(t_hi - 1), err(e) {}
+  __device__ long long next() {
+    const int u = min(t, last);
+    t += kTile;
+    if (c.page_size == 0) return base + u;
+    const int i = u / c.page_size;
+    int pg = __ldg(table + i);
+    if (pg < 0 || pg >= c.num_pages) {
+      if (err) atomicOr(err, kDevErrBadPage);
+      pg = 0;
+    }
+    return (static_cast<long long>(pg) * c.Hkv + kv) * c.page_size + (u - i * c.page_size);
+  }
+};
 
 // 32 mask bits of new token i's row from bit a (new-token index of the first; bits below 0
 // are the prefix: seen)
@@ -384,6 +423,117 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int wpr, int 
   return __funnelshift_r(mask_word(row, wpr, i, k), mask_word(row, wpr, i, k + 1), a & 31);
 }
 
+// Running maximum (log2 units), sum of the truncated weights, sum of the exact ones.
+struct RowState {
+  float m, l, lx;
+};
+
+// The rows whose maximum rises (to `top`; the others pass their m): their sums and their
+// accumulator scaled to it.
+template <int D>
+__device__ __forceinline__ RowState raise_max(RowState st, float top, uint32_t to, bool have_o) {
+  const float a = st.m == -INFINITY ? 0.0f : ex2(st.m - top);
+  st.l *= a;
+  st.lx *= a;
+  st.m = top;
+  if (have_o) {
+#pragma unroll 1
+    for (int o = 0; o < D; o += 4) {  // few registers: a whole row of logits is held meanwhile
+      uint32_t w[4];
+      tc_ld4(to + o, w);
+      tc_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * a);
+      tc_st4(to + o, w);
+    }
+    tc_wait_st();
+  }
+  return st;
+}
+
+// Half h of a tile: 64 logits of this thread's row (times f: log2 units) to weights, written
+// over them two to a column.  All 64 are in registers before the first
+// exponential, so that these run back to back.  `busy`: a barrier to wait for before the
+// accumulator is touched (0: none); false when that wait gives up.
+template <int D>
+__device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, int h, float f, const float* col, bool tail,
+                                             uint32_t bits0, uint32_t bits1, RowState& st, bool have_o, uint32_t busy,
+                                             uint32_t parity, bool want_lse) {
+  constexpr int N = kTile / 2;
+  float s[N];
+  {
+    uint32_t u0[32], u1[32];
+    tc_ld32(ts + N * h, u0);
+    tc_ld32(ts + N * h + 32, u1);
+    tc_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      s[j] = __uint_as_float(u0[j]);
+      s[32 + j] = __uint_as_float(u1[j]);
+    }
+  }
+  if (tail) {  // each token has its own scale, and is masked
+#pragma unroll
+    for (int j = 0; j < N; ++j) s[j] = ((j < 32 ? bits0 : bits1) >> (j & 31)) & 1u ? s[j] * col[N * h + j] : -INFINITY;
+  }
+  float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int j = 4; j < N; j += 8) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      mx[e] = j + e + 4 < N ? max3(mx[e], s[j + e], s[j + e + 4]) : fmaxf(mx[e], s[j + e]);
+  }
+  const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * f;
+  const bool raise = top > st.m + kLazy;
+  bool ok = true;
+  if (__any_sync(kAll, raise)) {
+    if (busy) ok = mbar_wait(busy, parity);
+    tc_fence_after();
+    st = raise_max<D>(st, raise ? top : st.m, to, have_o);
+  }
+  const float mm = st.m == -INFINITY ? 0.0f : st.m;
+  const uint64_t f2 = codec::pk2(f, f), m2 = codec::pk2(-mm, -mm);
+  uint64_t a[2] = {0ull, 0ull};
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint64_t y = codec::fma2(codec::pk2(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), f2, m2);
+      const float e0 = ex2(codec::pk_lo(y)), e1 = ex2(codec::pk_hi(y));
+      const uint32_t h0 = __float_as_uint(e0) & 0xffff0000u, h1 = __float_as_uint(e1) & 0xffff0000u;
+      w[j] = __byte_perm(h0, h1, 0x7632);
+      a[j & 1] = codec::add2(a[j & 1], codec::pk2(__uint_as_float(h0), __uint_as_float(h1)));
+      if (want_lse) st.lx += e0 + e1;
+    }
+    tc_st16(ts + N * h + 16 * c, w);
+  }
+  const uint64_t t = codec::add2(a[0], a[1]);
+  st.l += codec::pk_lo(t) + codec::pk_hi(t);
+  tc_wait_st();
+  return ok;
+}
+
+// The sum of channel `ch` over the new tokens that row i sees and whose value there is not
+// finite once rounded to bf16 (they were left out of the value tiles).
+template <bool V2, bool PAIR>
+__device__ __forceinline__ float bad_values(const TreeParams& p, const uint32_t* words, int wpr, int i, int b, int kv,
+                                         int lo, int t_lo, int t_hi, int P, int wl, int ch) {
+  float sum = 0.0f;
+  const int d = p.c.d, ng = d / 32;
+#pragma unroll 1
+  for (int tt = lo; tt < t_hi; ++tt) {
+    if (!PAIR && (((tt - t_lo) / kTile) & 1) != wl) continue;
+    if (!((mask_word(words, wpr, i, (tt - P) >> 5) >> ((tt - P) & 31)) & 1u)) continue;
+    const size_t row = cache_row_read(p.c, b, kv, tt, p.err);
+    const float v = V2 ? fmaf(static_cast<float>(code2(p.c.v_codes + row * (d / 4), ch)),
+                              p.c.v_scale[row * ng + ch / 32], p.c.v_min[row * ng + ch / 32])
+                       : load_elem(p.c.v, row * d + ch, true);
+    if (!(fabsf(v) < 0x1.FFp127f)) sum += v;
+  }
+  return sum;
+}
+
 template <int D, int R, bool V2, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUtensorMap vmap) {
@@ -392,7 +542,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   constexpr int VS = Ly::kVStages;
   extern __shared__ uint8_t raw_smem[];
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
   const int unit = blockIdx.z, b = unit / p.c.Hkv, kv = unit - b * p.c.Hkv;
   const SpanSeq sq = span_seq(p.span, b);
   const int rows = sq.n * p.G, xb = blockIdx.x * (PAIR ? 2 : 1) * kBlock;
@@ -432,9 +582,10 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   auto k_empty = [&](int s) { return bars + 8 * (1 + kKStages + s); };
   auto v_full = [&](int s) { return bars + 8 * (1 + 2 * kKStages + s); };
   auto v_empty = [&](int s) { return bars + 8 * (1 + 2 * kKStages + VS + s); };
-  auto s_full = [&](int l) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + l); };
-  auto p_full = [&](int l) { return bars + 8 * (3 + 2 * kKStages + 2 * VS + l); };
-  auto o_done = [&](int l) { return bars + 8 * (5 + 2 * kKStages + 2 * VS + l); };
+  // per lane l and half h (64 tokens) of its tile: logits written, weights written, readout done
+  auto s_full = [&](int l, int h) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + 2 * l + h); };
+  auto p_full = [&](int l, int h) { return bars + 8 * (5 + 2 * kKStages + 2 * VS + 2 * l + h); };
+  auto o_done = [&](int l, int h) { return bars + 8 * (9 + 2 * kKStages + 2 * VS + 2 * l + h); };
 
   // tiles of lane l: PAIR all of them (when the lane has rows), else those of its parity
   const int lanes_on = PAIR ? (xb + kBlock < rows ? 2 : 1) : (tiles > 1 ? 2 : 1);
@@ -444,18 +595,20 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   if (tid == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < kKStages; ++s) {
-      mbar_init(k_full(s), 4);
+      mbar_init(k_full(s), 8);
       mbar_init(k_empty(s), PAIR ? lanes_on : 1);
     }
     for (int s = 0; s < VS; ++s) {
-      mbar_init(v_full(s), V2 ? 4 : 1);
+      mbar_init(v_full(s), V2 ? 8 : 1);
       mbar_init(v_empty(s), PAIR ? lanes_on : 1);
     }
     for (int l = 0; l < 2; ++l) {
       const int r0 = rows - xb - (PAIR ? l * kBlock : 0);
-      mbar_init(s_full(l), 1);
-      mbar_init(p_full(l), max(1, min(4, (r0 + 31) / 32)));  // warps that have rows
-      mbar_init(o_done(l), 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(s_full(l, h), 1);
+        mbar_init(p_full(l, h), max(1, min(4, (r0 + 31) / 32)));  // warps that have rows
+        mbar_init(o_done(l, h), 1);
+      }
     }
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -471,6 +624,9 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
   bool ok = true;
 
+  // Registers move from the other warps to the softmax warps, a warpgroup at a time.
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kTmaWarp) {
     if (lane == 0) {
       const int nq = PAIR ? lanes_on : 1;
@@ -498,136 +654,135 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       }
       if (!mbar_wait(q_full, 0)) ok = false;
     }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      constexpr uint32_t kLogit = mma_desc(0, 0, kTile);       // fp16, both operands K-major
-      constexpr uint32_t kRead = mma_desc(1, 1, D);            // bf16, values channel-major
-      ok = mbar_wait(q_full, 0);
-      int k[2] = {0, 0};
-      bool have_s[2] = {false, false};
-      long long start = clock64();
-      while (ok && (k[0] < lane_tiles(0) || k[1] < lane_tiles(1))) {
-        bool moved = false;
+  } else if (warp < kTmaWarp) {
+    // The halves of a lane's tile take turns: while the exponentials of one run, the other's
+    // readout and next logits do.
+    const int l = warp - kMmaWarp, n = lane_tiles(l);
+    constexpr uint32_t kLogit = mma_desc(0, 0, kTile / 2);  // fp16, both operands K-major
+    constexpr uint32_t kRead = mma_desc(1, 1, D);           // bf16, values channel-major
+    constexpr uint32_t kSwz = desc_hi(1024, 2), kFlat = desc_hi(128, 0);
+    constexpr uint32_t kSide = D / 64 * (kTile * 128);  // the side entries within an operand
+    const uint32_t one = lane == 0;
+    const uint32_t qa = base + Ly::kQ + (PAIR ? l * Ly::kOperand : 0);
+    const uint32_t q_lo = desc_lo(qa, 16), qs_lo = desc_lo(qa + kSide, kTile * 16);
+    const uint32_t k_lo = desc_lo(base + Ly::kK, 16), ks_lo = desc_lo(base + Ly::kK + kSide, kTile * 16);
+    const uint32_t v_lo = desc_lo(base + Ly::kV, kTile * 128);
+    auto wait = [&](uint32_t bar, int phase) {
+      ok = __all_sync(kAll, ok && mbar_wait(bar, phase & 1));
+      return ok;
+    };
+    // step -1: logits of tile 0; step k: readout of tile k, each half followed by its logits
+    // of tile k + 1, which overwrite the weights it read
+    if (n > 0) wait(q_full, 0);
+#pragma unroll 1
+    for (int x = -2; x < 2 * n && ok; ++x) {
+      const int k = x >> 1, h = x & 1;
+      if (k >= 0) {
+        const int tile = tile_of(l, k), s = tile % VS;
+        if (!wait(p_full(l, h), k) || !wait(v_full(s), tile / VS)) break;
+        tc_fence_after();
+        const uint32_t va = v_lo + ((s * Ly::kVTile + 8192 * h) >> 4), w = tmem + 128 * l + 64 * h;
 #pragma unroll
-        for (int l = 0; l < 2; ++l) {
-          if (k[l] >= lane_tiles(l)) continue;
-          const int tile = tile_of(l, k[l]);
-          if (!have_s[l]) {  // logits of the lane's next tile, once its last readout is done
-            const int s = tile % kKStages;
-            if (k[l] > 0 && !mbar_test(o_done(l), (k[l] - 1) & 1)) continue;
-            if (!mbar_test(k_full(s), (tile / kKStages) & 1)) continue;
-            tc_fence_after();
-            const uint32_t qa = base + Ly::kQ + (PAIR ? l * Ly::kOperand : 0), ka = base + Ly::kK + s * Ly::kOperand;
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                tc_mma_ss(tmem + 128 * l, smem_desc(qa + c * (kTile * 128) + 32 * e, 16, 1024, 2),
-                          smem_desc(ka + c * (kTile * 128) + 32 * e, 16, 1024, 2), kLogit, c + e > 0);
-            if constexpr (R > 0)
-              tc_mma_ss(tmem + 128 * l, smem_desc(qa + D / 64 * (kTile * 128), kTile * 16, 128, 0),
-                        smem_desc(ka + D / 64 * (kTile * 128), kTile * 16, 128, 0), kLogit, true);
-            tc_commit(s_full(l));
-            tc_commit(k_empty(s));
-            have_s[l] = true;
-            moved = true;
-          } else {  // readout of the lane's tile
-            const int s = tile % VS;
-            if (!mbar_test(p_full(l), k[l] & 1) || !mbar_test(v_full(s), (tile / VS) & 1)) continue;
-            tc_fence_after();
-            const uint32_t va = base + Ly::kV + s * Ly::kVTile;
-#pragma unroll
-            for (int e = 0; e < kTile / 16; ++e)
-              tc_mma_ts(tmem + 256 + 128 * l, tmem + 128 * l + 8 * e, smem_desc(va + 2048 * e, kTile * 128, 1024, 2),
-                        kRead, k[l] > 0 || e > 0);
-            tc_commit(o_done(l));
-            tc_commit(v_empty(s));
-            have_s[l] = false;
-            ++k[l];
-            moved = true;
-          }
-        }
-        if (moved) start = clock64();
-        else if (clock64() - start > dc::kWaitCycles) ok = false;
+        for (int e = 0; e < 4; ++e)
+          tc_mma_ts(tmem + 256 + 128 * l, w + 8 * e, va + (2048 >> 4) * e, kSwz, kRead, x > 0 || e > 0, one);
+        tc_commit(o_done(l, h), one);
+        if (h == 1) tc_commit(v_empty(s), one);
       }
-      // the products are done before TMEM is given back
-      for (int l = 0; l < 2; ++l)
-        if (k[l] > 0 && !mbar_wait(o_done(l), (k[l] - 1) & 1)) ok = false;
+      if (k + 1 < n) {
+        const int tile = tile_of(l, k + 1), s = tile % kKStages;
+        if ((k >= 0 && !wait(o_done(l, h), k)) || !wait(k_full(s), tile / kKStages)) break;
+        tc_fence_after();
+        const uint32_t ka = (s * Ly::kOperand + 8192 * h) >> 4, d = tmem + 128 * l + 64 * h;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          const uint32_t off = ((e >> 2) * (kTile * 128) + 32 * (e & 3)) >> 4;
+          tc_mma_ss(d, q_lo + off, kSwz, k_lo + ka + off, kSwz, kLogit, e > 0, one);
+        }
+        if constexpr (R > 0)
+          tc_mma_ss(d, qs_lo, kFlat, ks_lo + ((s * Ly::kOperand + 1024 * h) >> 4), kFlat, kLogit, true, one);
+        tc_commit(s_full(l, h), one);
+        if (h == 1) tc_commit(k_empty(s), one);
+      }
     }
+    // the products are done before TMEM is given back
+    if (n > 0 && ok) wait(o_done(l, 1), n - 1);
+    __syncwarp();
+  }
   } else if (warp >= kDecodeWarp) {
-    const int tok = tid - kDecodeWarp * 32;
-    float* red = reinterpret_cast<float*>(misc + 4);  // [2][4] warp maxima
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
+    const int tok = (tid - kDecodeWarp * 32) & (kTile - 1), half = (warp - kDecodeWarp) >> 2;
+    float* red = reinterpret_cast<float*>(misc + 4);  // [2][8] warp maxima
+    constexpr int HG = NG / 2;  // groups of this half
+    TokenRows rows_of(p.c, b, kv, t_lo + tok, t_hi, p.err);
     RawToken<D, R, V2> cur, nxt;
-    load_token<D, R, V2>(p, b, kv, t_lo + tok, t_hi, cur);
+    load_token<D, R, V2>(p.c, rows_of.next(), half, cur);
+    long long row = rows_of.next();
+    // byte offset of chunk j of this half's 16-byte chunks in an operand's row
+    auto at = [&](int j) { return D == 128 ? half * (kTile * 128) + swz(tok, j) : swz(tok, 4 * half + j); };
     for (int k = 0; k < tiles; ++k) {
       const int t0 = t_lo + k * kTile, s = k % kKStages, sv = k % VS;
-      if (k + 1 < tiles) load_token<D, R, V2>(p, b, kv, t0 + kTile + tok, t_hi, nxt);
+      load_token<D, R, V2>(p.c, row, half, nxt);
+      row = rows_of.next();
       const bool tail = t0 + kTile > min(P, t_hi);  // holds new tokens, or ends the sequence
       float mx = 7.0f * fabsf(cur.zs);
 #pragma unroll
       for (int g = 0; g < NG; ++g)
-        mx = fmaxf(mx, fmaxf(fabsf(cur.km[g]), fabsf(fmaf(3.0f, cur.ks[g], cur.km[g]))));
-      if (!tail) {  // one power of two per tile
+        mx = max3(mx, fabsf(cur.km[g]), fabsf(fmaf(3.0f, cur.ks[g], cur.km[g])));
+      if (!tail) {  // one power of two per tile; else one per token: an unseen new token's size touches no other
         const uint32_t w = __reduce_max_sync(kAll, __float_as_uint(mx));
-        if (lane == 0) red[(k & 1) * 4 + warp - kDecodeWarp] = __uint_as_float(w);
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        const float4 m4 = *reinterpret_cast<const float4*>(red + (k & 1) * 4);
+        if (lane == 0) red[(k & 1) * 8 + warp - kDecodeWarp] = __uint_as_float(w);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float4 m4 = *reinterpret_cast<const float4*>(red + (k & 1) * 8);  // half 0's four have them all
         mx = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-      } else {  // one per token: an unseen new token's size touches no other
-        asm volatile("bar.sync 1, 128;" ::: "memory");
       }
       const float2 sc = operand_scale(mx);
       if (k >= kKStages && ok && !mbar_wait(k_empty(s), ((k / kKStages) - 1) & 1)) ok = false;
-      scale_s[(k % kRing) * kTile + tok] = sc.y;
+      if (half == 0) scale_s[(k % kRing) * kTile + tok] = sc.y;
       uint8_t* ks = sm + Ly::kK + s * Ly::kOperand;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const float m = cur.km[g], d = cur.ks[g];
-        const uint32_t l01 = pack_f16(m * sc.x, fmaf(1.0f, d, m) * sc.x);
-        const uint32_t l23 = pack_f16(fmaf(2.0f, d, m) * sc.x, fmaf(3.0f, d, m) * sc.x);
+      for (int g = 0; g < HG; ++g) {
+        const float m = (half ? cur.km[HG + g] : cur.km[g]) * sc.x, d = (half ? cur.ks[HG + g] : cur.ks[g]) * sc.x;
+        const uint32_t l01 = pack_f16(m, m + d), l23 = pack_f16(fmaf(2.0f, d, m), fmaf(3.0f, d, m));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint4 a, c;
-          pick16(word_of(cur.kc[g / 2], 2 * (g & 1) + h), l01, l23, a, c);
-          *reinterpret_cast<uint4*>(ks + swz(tok, 4 * g + 2 * h)) = a;
-          *reinterpret_cast<uint4*>(ks + swz(tok, 4 * g + 2 * h + 1)) = c;
+          pick16(cur.kw[2 * g + h], l01, l23, a, c);
+          *reinterpret_cast<uint4*>(ks + at(4 * g + 2 * h)) = a;
+          *reinterpret_cast<uint4*>(ks + at(4 * g + 2 * h + 1)) = c;
         }
       }
       if constexpr (R > 0) {
         const float zs = cur.zs * sc.x;
-        uint4* zb = reinterpret_cast<uint4*>(ks + D / 64 * (kTile * 128));
+        uint32_t o[4] = {0, 0, 0, 0};
+        if (8 * half < R) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t o[4] = {0, 0, 0, 0};
-          if (h < R / 8) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // nibble ^ 8 is w + 8; 2^23 + that has it in its low mantissa bits
-              const uint32_t w = cur.zc[h < R / 8 ? h : 0] >> (8 * e);
-              const float a = __uint_as_float(0x4B000000u | ((w & 15u) ^ 8u)) - 8388616.0f;
-              const float c = __uint_as_float(0x4B000000u | (((w >> 4) & 15u) ^ 8u)) - 8388616.0f;
-              o[e] = pack_f16(a * zs, c * zs);
-            }
+          for (int e = 0; e < 4; ++e) {
+            // nibble ^ 8 is w + 8; 2^23 + that has it in its low mantissa bits
+            const uint32_t w = cur.zc >> (8 * e);
+            const float a = __uint_as_float((w & 15u) ^ 0x4B000008u) - 8388616.0f;
+            const float c = __uint_as_float(((w >> 4) & 15u) ^ 0x4B000008u) - 8388616.0f;
+            o[e] = pack_f16(a * zs, c * zs);
           }
-          zb[h * kTile + tok] = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        reinterpret_cast<uint4*>(ks + D / 64 * (kTile * 128))[half * kTile + tok] = make_uint4(o[0], o[1], o[2], o[3]);
       }
       if constexpr (V2) {
         if (k >= VS && ok && !mbar_wait(v_empty(sv), ((k / VS) - 1) & 1)) ok = false;
         uint8_t* vs = sm + Ly::kV + sv * Ly::kVTile;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < HG; ++g) {
           const float m = cur.vm[g], d = cur.vs[g];
-          uint32_t l01 = pack_bf16(m, fmaf(1.0f, d, m)), l23 = pack_bf16(fmaf(2.0f, d, m), fmaf(3.0f, d, m));
+          uint32_t l01 = pack_bf16(m, m + d), l23 = pack_bf16(fmaf(2.0f, d, m), fmaf(3.0f, d, m));
           // a new token's value that is not finite must not meet the zero weights of the
           // rows that do not see it: it is left out here and added to the rows that do
+          if (t0 + tok >= t_hi) l01 = l23 = 0u;
           if (t0 + tok >= P && (drop_bad(l01) | drop_bad(l23))) misc[1] = 1u;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint4 a, c;
-            pick16(word_of(cur.vc[g / 2], 2 * (g & 1) + h), l01, l23, a, c);
-            *reinterpret_cast<uint4*>(vs + swz(tok, 4 * g + 2 * h)) = a;
-            *reinterpret_cast<uint4*>(vs + swz(tok, 4 * g + 2 * h + 1)) = c;
+            pick16(cur.vw[2 * g + h], l01, l23, a, c);
+            *reinterpret_cast<uint4*>(vs + at(4 * g + 2 * h)) = a;
+            *reinterpret_cast<uint4*>(vs + at(4 * g + 2 * h + 1)) = c;
           }
         }
       } else if (tail) {
@@ -636,8 +791,9 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         uint8_t* vs = sm + Ly::kV + sv * Ly::kVTile;
         if (t0 + tok >= P) {
           const bool past = t0 + tok >= t_hi;
-          for (int c = 0; c < D / 8; ++c) {
-            uint32_t* w = reinterpret_cast<uint32_t*>(vs + swz(tok, c));
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(vs + at(c));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t v = past ? 0u : w[e];
@@ -655,7 +811,9 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       }
       cur = nxt;
     }
-  } else if (xb + (PAIR ? wl * kBlock : 0) + (warp & 3) * 32 < rows && wl < lanes_on) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+  if (xb + (PAIR ? wl * kBlock : 0) + (warp & 3) * 32 < rows && wl < lanes_on) {
     // ---- softmax and epilogue of this warp's 32 query rows
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + 128 * wl + lane_off, to = tmem + 256 + 128 * wl + lane_off;
@@ -663,88 +821,35 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     const float fq = t.qf[static_cast<size_t>(unit) * t.blocks * kBlock + x];
     const uint32_t* words = t.words ? t.words + (static_cast<size_t>(b) * p.span.n + i) * t.wpr : nullptr;
     const bool want_lse = p.lse != nullptr;
-    float m = -INFINITY, l = 0.0f, lx = 0.0f;
+    RowState st{-INFINITY, 0.0f, 0.0f};
     const int nk = lane_tiles(wl);
     for (int k = 0; k < nk; ++k) {
       const int tile = tile_of(wl, k), t0 = t_lo + tile * kTile;
-      if (!mbar_wait(s_full(wl), k & 1)) { ok = false; break; }
-      tc_fence_after();
       const float* col = scale_s + (tile % kRing) * kTile;
       const bool tail = t0 + kTile > min(P, t_hi);
-      const float f = fmaxf(tail ? fq : fq * col[0], 1e-37f);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t sr[32];
-        tc_ld32(ts + 32 * c, sr);
-        tc_wait_ld();
-        float s[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(sr[j]);
+#pragma unroll 1
+      for (int h = 0; h < 2 && ok; ++h) {
+        uint32_t b0 = 0u, b1 = 0u;
         if (tail) {
-          const uint32_t bits = mask_bits(words, t.wpr, i, t0 + 32 * c - P);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) s[j] = (bits >> j) & 1u ? s[j] * col[32 * c + j] : -INFINITY;
+          b0 = mask_bits(words, t.wpr, i, t0 + 64 * h - P);
+          b1 = mask_bits(words, t.wpr, i, t0 + 64 * h + 32 - P);
         }
-        float mx = s[0];
-#pragma unroll
-        for (int j = 1; j < 32; ++j) mx = fmaxf(mx, s[j]);
-        const float top = mx * f;
-        const bool raise = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
-        if (__any_sync(kAll, raise)) {
-          const float m2 = raise ? top : m;
-          const float a = m == -INFINITY ? 0.0f : ex2(m - m2);
-          l *= a;
-          lx *= a;
-          m = m2;
-          if (k > 0) {
-#pragma unroll
-            for (int o = 0; o < D; o += 16) {
-              uint32_t w[16];
-              tc_ld16(to + o, w);
-              tc_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * a);
-              tc_st16(to + o, w);
-            }
-          }
-          for (int o = 0; o < c; ++o) {  // this tile's weights so far
-            uint32_t w[16];
-            tc_ld16(ts + 16 * o, w);
-            tc_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float e0 = __uint_as_float(w[j] << 16) * a, e1 = __uint_as_float(w[j] & 0xffff0000u) * a;
-              const uint32_t h0 = __float_as_uint(e0) & 0xffff0000u, h1 = __float_as_uint(e1) & 0xffff0000u;
-              l += (__uint_as_float(h0) - e0) + (__uint_as_float(h1) - e1);
-              w[j] = (h0 >> 16) | h1;
-            }
-            tc_st16(ts + 16 * o, w);
-          }
-          tc_wait_st();
-        }
-        const float mm = m == -INFINITY ? 0.0f : m;
-        const uint64_t f2 = codec::pk2(f, f), m2 = codec::pk2(-mm, -mm);
-        uint32_t w[16];
-        uint64_t sum = 0ull, sumx = 0ull;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint64_t y = codec::fma2(codec::pk2(s[2 * j], s[2 * j + 1]), f2, m2);
-          const float e0 = ex2(codec::pk_lo(y)), e1 = ex2(codec::pk_hi(y));
-          const uint32_t h0 = __float_as_uint(e0) & 0xffff0000u, h1 = __float_as_uint(e1) & 0xffff0000u;
-          w[j] = __byte_perm(h0, h1, 0x7632);
-          sum = codec::add2(sum, codec::pk2(__uint_as_float(h0), __uint_as_float(h1)));
-          if (want_lse) sumx = codec::add2(sumx, codec::pk2(e0, e1));
-        }
-        l += codec::pk_lo(sum) + codec::pk_hi(sum);
-        lx += codec::pk_lo(sumx) + codec::pk_hi(sumx);
-        tc_st16(ts + 16 * c, w);
+        if (!mbar_wait(s_full(wl, h), k & 1)) { ok = false; break; }
+        tc_fence_after();
+        const float f = fmaxf(tail ? fq : fq * col[0], 1e-37f);
+        // the accumulator rests once the half before this one is read out
+        const bool have_o = k > 0 || h > 0;
+        if (!softmax_half<D>(ts, to, h, f, col, tail, b0, b1, st, have_o, have_o ? o_done(wl, 1 - h) : 0u,
+                             (h ? k : k - 1) & 1, want_lse))
+          ok = false;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(wl, h));
       }
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(wl));
+      if (!ok) break;
     }
-    if (ok && nk > 0 && !mbar_wait(o_done(wl), (nk - 1) & 1)) ok = false;
+    const float m = st.m, l = st.l, lx = st.lx;
+    if (ok && nk > 0 && !mbar_wait(o_done(wl, 1), (nk - 1) & 1)) ok = false;
     tc_fence_after();
     if (ok) {
       const bool bad = *reinterpret_cast<volatile uint32_t*>(misc + 1) != 0u;
@@ -754,7 +859,20 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       const int h = kv * p.G + x - i * p.G;
       const size_t orow = static_cast<size_t>(sq.row0) + i;
       const float inv = !direct ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
+      if (bad) {  // rare: one column at a time, in TMEM
+#pragma unroll 1
+        for (int c = 0; c < D; ++c) {
+          const float add = bad_values<V2, PAIR>(p, words, t.wpr, i, b, kv, max(P, t_lo), t_lo, t_hi, P, wl,
+                                                 V2 ? channel_at(c) : c);
+          uint32_t w;
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(w) : "r"(to + c));
+          tc_wait_ld();
+          w = __float_as_uint(__uint_as_float(w) + add);
+          asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(to + c), "r"(w) : "memory");
+        }
+        tc_wait_st();
+      }
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t w[32];
         tc_ld32(to + 32 * c, w);
@@ -765,22 +883,6 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         if (l == 0.0f) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-        }
-        if (bad && x < rows) {  // values that are not finite, for the rows that see them
-          for (int tt = max(P, t_lo); tt < t_hi; ++tt) {
-            const int tl = (tt - t_lo) / kTile;
-            if (!PAIR && (tl & 1) != wl) continue;
-            if (!((mask_word(words, t.wpr, i, (tt - P) >> 5) >> ((tt - P) & 31)) & 1u)) continue;
-            const size_t row = cache_row_read(p.c, b, kv, tt, p.err);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int ch = 32 * c + j;
-              const float v = V2 ? fmaf(static_cast<float>(code2(p.c.v_codes + row * (D / 4), ch)),
-                                        p.c.v_scale[row * NG + c], p.c.v_min[row * NG + c])
-                                 : load_elem(p.c.v, row * D + ch, true);
-              if (!(fabsf(v) < 0x1.FFp127f)) o[j] += v;  // not finite once rounded to bf16
-            }
-          }
         }
         if (x < rows) {
 #pragma unroll
@@ -796,10 +898,11 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         else if (want_lse) p.lse[orow * p.Hq + h] = l == 0.0f ? -INFINITY : m * dc::kLn2 + logf(lx);
       }
     }
-  } else if (warp < 8 && x < rows && !PAIR && wl < lane_parts) {
+  } else if (x < rows && !PAIR && wl < lane_parts) {
     // the lane without a tile: its split is empty
     p.part_ml[(static_cast<size_t>(unit) * p.splits + blockIdx.y * lane_parts + wl) * part_rows + x] =
         make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+  }
   }
 
   if (!ok) atomicOr(p.err, kDevErrWaitTimeout);
