@@ -23,9 +23,10 @@
 //   2 x 4 softmax warps (two "lanes"), one thread per query row.  PAIR (more than 128 rows):
 //     the lanes hold two row blocks over the same tiles, so each decoded tile serves 256
 //     rows; else they take alternate tiles of the one block and end as two splits.
-// The running maximum is refreshed lazily (when a logit exceeds it by 2^40): one pass over
-// the logits, and the output accumulator in TMEM is rescaled only then, which peaked
-// attention would do for some row of a warp in a third of the 32-token steps at 2^8.  Weights are
+// The running maximum is kept with a slack of 2^40 (kSlack): one pass over the logits and no
+// search for the maximum in it, and the output accumulator in TMEM is rescaled only when a
+// weight reaches 2, which is rare (with a slack of 2^8 it was a third of the steps in peaked
+// attention).  Weights are
 // truncated to bf16 and the sum is taken over the truncated weights, so that the error of
 // a weight cancels where one token holds most of it; the log-sum-exp, when asked for, is
 // summed over the unrounded ones.
@@ -54,10 +55,11 @@ constexpr int kRegsSoftmax = 128, kRegsDecode = 80, kRegsOther = 48;
 constexpr int kDecodeWarp = 8, kMmaWarp = 16, kTmaWarp = 18;  // one MMA warp per lane
 constexpr int kKStages = 2;
 constexpr int kRing = 8;            // tiles whose key scales are kept (more than can be in flight)
-// log2 units by which a logit may exceed the running maximum before that is raised.  Weights,
-// sums and accumulators all have the 8-bit exponent of fp32, so a weight of 2^40 costs no
-// precision; sums stay finite for values below 2^70.
-constexpr float kLazy = 40.0f;
+// A row's weights are 2^(logit - m) with m at least the largest logit so far and, when it is
+// set, kSlack above it: the check that a step stays below 2 is then one bit of the weights,
+// and m is seldom set again.  Weights, sums and accumulators all have the 8-bit exponent of
+// fp32, so the offset costs no precision (a weight 2^-86 of the largest is still normal).
+constexpr float kSlack = 40.0f;
 constexpr uint32_t kAll = 0xffffffffu;
 
 // bytes of 128 operand rows: d channels in 64-channel blocks (128-byte rows, 128-byte
@@ -96,7 +98,9 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, ui
       "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
+template <int N>
+__device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&v)[N], int o) {
+  uint32_t* r = v + o;
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -105,6 +109,14 @@ __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a));
+}
+__device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(a));
 }
 __device__ __forceinline__ void tc_ld4(uint32_t a, uint32_t (&r)[4]) {
@@ -117,7 +129,9 @@ __device__ __forceinline__ void tc_st4(uint32_t a, const uint32_t (&r)[4]) {
                "r"(r[3]), "r"(a)
                : "memory");
 }
-__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16]) {
+template <int N>
+__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&v)[N], int o) {
+  const uint32_t* r = v + o;
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
@@ -127,16 +141,40 @@ __device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// Wait for the phase of the given parity; false after about 2 s (every try suspends the warp
-// for a while by itself).  Short: it is in many places, and five roles share the SM's
-// instruction cache.
+// A try that the hardware itself suspends for a while.  (With a time hint the compiler puts
+// a loop of sleeps around it, whose instructions and wake-up times cost this kernel a third
+// of its issue slots.)
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Wait for the phase of the given parity; false after about 2 s.  Short: it is in many
+// places, and five roles share the SM's instruction cache.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-  if (dc::mbar_try_wait(bar, parity)) return true;
+  if (mbar_try(bar, parity)) return true;
   const long long start = clock64();
+  do {
 #pragma unroll 1
-  while (!dc::mbar_try_wait(bar, parity))
-    if (clock64() - start > dc::kWaitCycles) return false;
-  return true;
+    for (int k = 0; k < 256; ++k)
+      if (mbar_try(bar, parity)) return true;
+  } while (clock64() - start < dc::kWaitCycles);
+  return false;
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -428,7 +466,7 @@ struct RowState {
   float m, l, lx;
 };
 
-// The rows whose maximum rises (to `top`; the others pass their m): their sums and their
+// The rows whose m rises (to `top`; the others pass their m): their sums and their
 // accumulator scaled to it.
 template <int D>
 __device__ __forceinline__ RowState raise_max(RowState st, float top, uint32_t to, bool have_o) {
@@ -438,7 +476,7 @@ __device__ __forceinline__ RowState raise_max(RowState st, float top, uint32_t t
   st.m = top;
   if (have_o) {
 #pragma unroll 1
-    for (int o = 0; o < D; o += 4) {  // few registers: a whole row of logits is held meanwhile
+    for (int o = 0; o < D; o += 4) {  // few registers: half a row of logits is held meanwhile
       uint32_t w[4];
       tc_ld4(to + o, w);
       tc_wait_ld();
@@ -451,67 +489,46 @@ __device__ __forceinline__ RowState raise_max(RowState st, float top, uint32_t t
   return st;
 }
 
-// Half h of a tile: 64 logits of this thread's row (times f: log2 units) to weights, written
-// over them two to a column.  All 64 are in registers before the first
-// exponential, so that these run back to back.  `busy`: a barrier to wait for before the
-// accumulator is touched (0: none); false when that wait gives up.
-template <int D>
-__device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, int h, float f, const float* col, bool tail,
-                                             uint32_t bits0, uint32_t bits1, RowState& st, bool have_o, uint32_t busy,
-                                             uint32_t parity, bool want_lse) {
-  constexpr int N = kTile / 2;
-  float s[N];
-  {
-    uint32_t u0[32], u1[32];
-    tc_ld32(ts + N * h, u0);
-    tc_ld32(ts + N * h + 32, u1);
+constexpr int kHalf = kTile / 2;
+
+// The logits of half a tile that holds new tokens or ends the sequence, in TMEM: each token
+// has its own scale, and is masked.  a: new-token index of the half's first token.
+__device__ __forceinline__ void mask_half(uint32_t ts, const uint32_t* row, int wpr, int i, int a, const float* col) {
+#pragma unroll 1
+  for (int c = 0; c < kHalf; c += 16) {
+    uint32_t w[16];
+    tc_ld16(ts + c, w);
+    const uint32_t bits = mask_bits(row, wpr, i, a + c);
     tc_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      s[j] = __uint_as_float(u0[j]);
-      s[32 + j] = __uint_as_float(u1[j]);
-    }
+    for (int j = 0; j < 16; ++j)
+      w[j] = __float_as_uint((bits >> j) & 1u ? __uint_as_float(w[j]) * col[c + j] : -INFINITY);
+    tc_st16(ts + c, w, 0);
   }
-  if (tail) {  // each token has its own scale, and is masked
-#pragma unroll
-    for (int j = 0; j < N; ++j) s[j] = ((j < 32 ? bits0 : bits1) >> (j & 31)) & 1u ? s[j] * col[N * h + j] : -INFINITY;
-  }
-  float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-  for (int j = 4; j < N; j += 8) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      mx[e] = j + e + 4 < N ? max3(mx[e], s[j + e], s[j + e + 4]) : fmaxf(mx[e], s[j + e]);
-  }
-  const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * f;
-  const bool raise = top > st.m + kLazy;
-  bool ok = true;
-  if (__any_sync(kAll, raise)) {
-    if (busy) ok = mbar_wait(busy, parity);
-    tc_fence_after();
-    st = raise_max<D>(st, raise ? top : st.m, to, have_o);
-  }
-  const float mm = st.m == -INFINITY ? 0.0f : st.m;
+  tc_wait_st();
+}
+
+// Half a tile's 64 logits of this thread's row (times f: log2 units) to weights, two to a
+// word; their sum, and all their bits.  The 64 are in registers before the first
+// exponential, so that these run back to back.
+__device__ __forceinline__ void weights(const uint32_t (&s)[kHalf], float f, float m, uint32_t (&w)[kHalf / 2],
+                                        float& sum, uint32_t& bits) {
+  const float mm = m == -INFINITY ? 0.0f : m;
   const uint64_t f2 = codec::pk2(f, f), m2 = codec::pk2(-mm, -mm);
   uint64_t a[2] = {0ull, 0ull};
+  uint32_t any[2] = {0u, 0u};
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint64_t y = codec::fma2(codec::pk2(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), f2, m2);
-      const float e0 = ex2(codec::pk_lo(y)), e1 = ex2(codec::pk_hi(y));
-      const uint32_t h0 = __float_as_uint(e0) & 0xffff0000u, h1 = __float_as_uint(e1) & 0xffff0000u;
-      w[j] = __byte_perm(h0, h1, 0x7632);
-      a[j & 1] = codec::add2(a[j & 1], codec::pk2(__uint_as_float(h0), __uint_as_float(h1)));
-      if (want_lse) st.lx += e0 + e1;
-    }
-    tc_st16(ts + N * h + 16 * c, w);
+  for (int j = 0; j < kHalf / 2; ++j) {
+    const uint64_t y = codec::fma2(codec::pk2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), f2, m2);
+    const uint32_t h0 = __float_as_uint(ex2(codec::pk_lo(y))) & 0xffff0000u;
+    const uint32_t h1 = __float_as_uint(ex2(codec::pk_hi(y))) & 0xffff0000u;
+    w[j] = __byte_perm(h0, h1, 0x7632);
+    any[j & 1] |= w[j];
+    a[j & 1] = codec::add2(a[j & 1], codec::pk2(__uint_as_float(h0), __uint_as_float(h1)));
   }
   const uint64_t t = codec::add2(a[0], a[1]);
-  st.l += codec::pk_lo(t) + codec::pk_hi(t);
-  tc_wait_st();
-  return ok;
+  sum = codec::pk_lo(t) + codec::pk_hi(t);
+  bits = any[0] | any[1];
 }
 
 // The sum of channel `ch` over the new tokens that row i sees and whose value there is not
@@ -675,8 +692,8 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     // of tile k + 1, which overwrite the weights it read
     if (n > 0) wait(q_full, 0);
 #pragma unroll 1
-    for (int x = -2; x < 2 * n && ok; ++x) {
-      const int k = x >> 1, h = x & 1;
+    for (int y = -2; y < 2 * n && ok; ++y) {
+      const int k = y >> 1, h = y & 1;
       if (k >= 0) {
         const int tile = tile_of(l, k), s = tile % VS;
         if (!wait(p_full(l, h), k) || !wait(v_full(s), tile / VS)) break;
@@ -684,7 +701,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         const uint32_t va = v_lo + ((s * Ly::kVTile + 8192 * h) >> 4), w = tmem + 128 * l + 64 * h;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          tc_mma_ts(tmem + 256 + 128 * l, w + 8 * e, va + (2048 >> 4) * e, kSwz, kRead, x > 0 || e > 0, one);
+          tc_mma_ts(tmem + 256 + 128 * l, w + 8 * e, va + (2048 >> 4) * e, kSwz, kRead, y > 0 || e > 0, one);
         tc_commit(o_done(l, h), one);
         if (h == 1) tc_commit(v_empty(s), one);
       }
@@ -728,15 +745,16 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
 #pragma unroll
       for (int g = 0; g < NG; ++g)
         mx = max3(mx, fabsf(cur.km[g]), fabsf(fmaf(3.0f, cur.ks[g], cur.km[g])));
+      const uint32_t wm = __reduce_max_sync(kAll, __float_as_uint(mx));
+      if (lane == 0) red[(k & 1) * 8 + warp - kDecodeWarp] = __uint_as_float(wm);
+      // one warp waits for the stage, the others for the barrier that they meet at anyway
+      if (warp == kDecodeWarp && k >= kKStages && ok && !mbar_wait(k_empty(s), ((k / kKStages) - 1) & 1)) ok = false;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
       if (!tail) {  // one power of two per tile; else one per token: an unseen new token's size touches no other
-        const uint32_t w = __reduce_max_sync(kAll, __float_as_uint(mx));
-        if (lane == 0) red[(k & 1) * 8 + warp - kDecodeWarp] = __uint_as_float(w);
-        asm volatile("bar.sync 1, 256;" ::: "memory");
         const float4 m4 = *reinterpret_cast<const float4*>(red + (k & 1) * 8);  // half 0's four have them all
         mx = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
       }
       const float2 sc = operand_scale(mx);
-      if (k >= kKStages && ok && !mbar_wait(k_empty(s), ((k / kKStages) - 1) & 1)) ok = false;
       if (half == 0) scale_s[(k % kRing) * kTile + tok] = sc.y;
       uint8_t* ks = sm + Ly::kK + s * Ly::kOperand;
 #pragma unroll
@@ -823,30 +841,67 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     const bool want_lse = p.lse != nullptr;
     RowState st{-INFINITY, 0.0f, 0.0f};
     const int nk = lane_tiles(wl);
-    for (int k = 0; k < nk; ++k) {
-      const int tile = tile_of(wl, k), t0 = t_lo + tile * kTile;
-      const float* col = scale_s + (tile % kRing) * kTile;
-      const bool tail = t0 + kTile > min(P, t_hi);
+    // One half-tile at a time; the next one's logits are on their way while this one's
+    // weights are written.
+    uint32_t s[kHalf];
+    float f = 0.0f;
+    const int tail_at = min(P, t_hi) >= t_lo ? (min(P, t_hi) - t_lo) / kTile : 0;  // tiles from here on hold new tokens or end the sequence
 #pragma unroll 1
-      for (int h = 0; h < 2 && ok; ++h) {
-        uint32_t b0 = 0u, b1 = 0u;
-        if (tail) {
-          b0 = mask_bits(words, t.wpr, i, t0 + 64 * h - P);
-          b1 = mask_bits(words, t.wpr, i, t0 + 64 * h + 32 - P);
+    for (int y = -1; y < 2 * nk && ok; ++y) {  // step y: half y & 1 of the lane's tile y / 2
+      const int h = y & 1;
+      if (y >= 0) {
+        tc_wait_ld();
+        uint32_t w[kHalf / 2], bits;
+        float sum;
+        weights(s, f, st.m, w, sum, bits);
+        // a weight of 2 or more (or not a number), or no m yet: find it, and the weights again
+        if (__any_sync(kAll, (bits & 0x40004000u) != 0u || y == 0)) {
+          float mx = __uint_as_float(s[0]);
+#pragma unroll
+          for (int j = 1; j < kHalf - 1; j += 2) mx = max3(mx, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+          const float top = fmaxf(mx, __uint_as_float(s[kHalf - 1])) * f;
+          // the accumulator rests once the half before this one is read out
+          if (y > 0 && !mbar_wait(o_done(wl, 1 - h), ((y - 1) >> 1) & 1)) ok = false;
+          tc_fence_after();
+          st = raise_max<D>(st, top > st.m ? top + kSlack : st.m, to, y > 0);
+          weights(s, f, st.m, w, sum, bits);
         }
-        if (!mbar_wait(s_full(wl, h), k & 1)) { ok = false; break; }
-        tc_fence_after();
-        const float f = fmaxf(tail ? fq : fq * col[0], 1e-37f);
-        // the accumulator rests once the half before this one is read out
-        const bool have_o = k > 0 || h > 0;
-        if (!softmax_half<D>(ts, to, h, f, col, tail, b0, b1, st, have_o, have_o ? o_done(wl, 1 - h) : 0u,
-                             (h ? k : k - 1) & 1, want_lse))
-          ok = false;
+        st.l += sum;
+        if (want_lse) {  // the unrounded weights once more, rather than their sums beside every other call's
+          const float mm = st.m == -INFINITY ? 0.0f : st.m;
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j) st.lx += ex2(fmaf(__uint_as_float(s[j]), f, -mm));
+        }
+        tc_st16(ts + kHalf * h, w, 0);
+        tc_st16(ts + kHalf * h + 16, w, 16);
+      }
+      auto hand_over = [&]() {
+        tc_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(wl, h));
+      };
+      bool handed = y < 0;
+      if (y + 1 < 2 * nk) {
+        const uint32_t bar = s_full(wl, 1 - h), parity = ((y + 1) >> 1) & 1;
+        if (!__all_sync(kAll, mbar_test(bar, parity))) {  // not there yet: this one's weights first
+          if (!handed) hand_over();
+          handed = true;
+          if (!mbar_wait(bar, parity)) ok = false;
+        }
+        const int tile = tile_of(wl, (y + 1) >> 1);
+        const float* col = scale_s + (tile % kRing) * kTile;
+        const uint32_t sa = ts + kHalf * (1 - h);
+        tc_fence_after();
+        f = fmaxf(fq * col[0], 1e-37f);
+        if (tile >= tail_at) {
+          f = fmaxf(fq, 1e-37f);
+          mask_half(sa, words, t.wpr, i, t_lo + tile * kTile + kHalf * (1 - h) - P, col + kHalf * (1 - h));
+        }
+        tc_ld32(sa, s, 0);
+        tc_ld32(sa + 32, s, 32);
       }
-      if (!ok) break;
+      if (!handed) hand_over();
     }
     const float m = st.m, l = st.l, lx = st.lx;
     if (ok && nk > 0 && !mbar_wait(o_done(wl, 1), (nk - 1) & 1)) ok = false;
@@ -875,7 +930,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t w[32];
-        tc_ld32(to + 32 * c, w);
+        tc_ld32(to + 32 * c, w, 0);
         tc_wait_ld();
         float o[32];  // in channel order
 #pragma unroll
