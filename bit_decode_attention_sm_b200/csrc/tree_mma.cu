@@ -11,7 +11,7 @@
 //   power of two (exact for bf16 queries but for elements 2^-28 below the row's largest),
 //   U_h^T q behind them, written as the shared-memory image the main kernel copies in; the
 //   mask as bits.
-// tree_mma_kernel    one CTA of 20 warps per (row blocks, split, sequence x KV head):
+// tree_mma_kernel    one CTA of 28 warps per (row blocks, split, sequence x KV head):
 //   8 decoder warps  two threads per token, half the channels each: packed codes from HBM (the next tile's loads in
 //     flight) to fp16 keys in shared memory, scaled by a power of two per tile.  The four
 //     levels min + code * scale of a 32-channel group are rounded to fp16 once, two 2-bit
@@ -20,7 +20,7 @@
 //     the same way in bf16.
 //   1 TMA warp       dense bf16 values, 64 tokens x 64 channels a box
 //   2 MMA warps      one per lane (below): logits into TMEM, readout from the weights there
-//   2 x 4 softmax warps (two "lanes"), one thread per query row.  PAIR (more than 128 rows):
+//   2 x 2 x 4 softmax warps: two "lanes", in each one thread per query row and half a tile.  PAIR (more than 128 rows):
 //     the lanes hold two row blocks over the same tiles, so each decoded tile serves 256
 //     rows; else they take alternate tiles of the one block and end as two splits.
 // The running maximum is kept with a slack of 2^40 (kSlack): one pass over the logits and no
@@ -48,11 +48,8 @@ using dc::smem_addr;
 
 constexpr int kTile = 128;          // tokens per tile
 constexpr int kBlock = 128;         // query rows per block
-constexpr int kThreads = 20 * 32;  // five whole warpgroups
-// registers per thread after the split: 8 x 32 x 128 + 8 x 32 x 80 + 4 x 32 x 48 = 59392, of
-// the 640 x 96 = 61440 that the block holds at launch
-constexpr int kRegsSoftmax = 128, kRegsDecode = 80, kRegsOther = 48;
-constexpr int kDecodeWarp = 8, kMmaWarp = 16, kTmaWarp = 18;  // one MMA warp per lane
+constexpr int kThreads = 28 * 32;   // seven whole warpgroups, at 72 registers a thread
+constexpr int kDecodeWarp = 16, kMmaWarp = 24, kTmaWarp = 26;  // one MMA warp per lane
 constexpr int kKStages = 2;
 constexpr int kRing = 8;            // tiles whose key scales are kept (more than can be in flight)
 // A row's weights are 2^(logit - m) with m at least the largest logit so far and, when it is
@@ -119,16 +116,6 @@ __device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t (&r)[16]) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(a));
 }
-__device__ __forceinline__ void tc_ld4(uint32_t a, uint32_t (&r)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a));
-}
-__device__ __forceinline__ void tc_st4(uint32_t a, const uint32_t (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0,%1,%2,%3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3]), "r"(a)
-               : "memory");
-}
 template <int N>
 __device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&v)[N], int o) {
   const uint32_t* r = v + o;
@@ -165,16 +152,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
       if (mbar_try(bar, parity)) return true;
   } while (clock64() - start < dc::kWaitCycles);
   return false;
-}
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -363,8 +340,10 @@ struct Layout {
   static constexpr int kK = kQ + (PAIR ? 2 : 1) * kOperand;
   static constexpr int kV = kK + kKStages * kOperand;
   static constexpr int kScale = kV + kVStages * kVTile;  // [kRing][kTile] floats
-  static constexpr int kBars = kScale + kRing * kTile * 4;
-  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 12;
+  static constexpr int kMax = kScale + kRing * kTile * 4;  // [2 lanes][kBlock] floats: m of each row
+  static constexpr int kSums = kMax + 2 * kBlock * 4;      // [2 lanes][2 halves][kBlock] float2: sums of each row
+  static constexpr int kBars = kSums + 4 * kBlock * 8;
+  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 12 + 16;
   static constexpr int kMisc = (kBars + 8 * kNumBars + 15) & ~15;  // tmem base, bad-value flag, 2 x 8 maxima
   static constexpr int kBytes = kMisc + 128 + 1024;    // and room for the alignment
 };
@@ -461,32 +440,19 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int wpr, int 
   return __funnelshift_r(mask_word(row, wpr, i, k), mask_word(row, wpr, i, k + 1), a & 31);
 }
 
-// Running maximum (log2 units), sum of the truncated weights, sum of the exact ones.
-struct RowState {
-  float m, l, lx;
-};
-
-// The rows whose m rises (to `top`; the others pass their m): their sums and their
-// accumulator scaled to it.
+// The accumulator of this thread's row times a.
 template <int D>
-__device__ __forceinline__ RowState raise_max(RowState st, float top, uint32_t to, bool have_o) {
-  const float a = st.m == -INFINITY ? 0.0f : ex2(st.m - top);
-  st.l *= a;
-  st.lx *= a;
-  st.m = top;
-  if (have_o) {
+__device__ __forceinline__ void scale_output(uint32_t to, float a) {
 #pragma unroll 1
-    for (int o = 0; o < D; o += 4) {  // few registers: half a row of logits is held meanwhile
-      uint32_t w[4];
-      tc_ld4(to + o, w);
-      tc_wait_ld();
+  for (int o = 0; o < D; o += 16) {
+    uint32_t w[16];
+    tc_ld16(to + o, w);
+    tc_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * a);
-      tc_st4(to + o, w);
-    }
-    tc_wait_st();
+    for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * a);
+    tc_st16(to + o, w, 0);
   }
-  return st;
+  tc_wait_st();
 }
 
 constexpr int kHalf = kTile / 2;
@@ -508,27 +474,42 @@ __device__ __forceinline__ void mask_half(uint32_t ts, const uint32_t* row, int 
   tc_wait_st();
 }
 
-// Half a tile's 64 logits of this thread's row (times f: log2 units) to weights, two to a
-// word; their sum, and all their bits.  The 64 are in registers before the first
-// exponential, so that these run back to back.
-__device__ __forceinline__ void weights(const uint32_t (&s)[kHalf], float f, float m, uint32_t (&w)[kHalf / 2],
-                                        float& sum, uint32_t& bits) {
+// 32 logits of this thread's row (times f: log2 units) to weights relative to 2^m, two to a
+// word (w + o); their sum, all their bits, and (exact) the sum of the unrounded ones.
+template <int N>
+__device__ __forceinline__ void weights32(uint32_t ts, float f, float m, uint32_t (&w)[N], int o, float& sum,
+                                          uint32_t& bits, bool want_exact, float& exact) {
+  uint32_t s[32];
+  tc_ld32(ts, s, 0);
   const float mm = m == -INFINITY ? 0.0f : m;
   const uint64_t f2 = codec::pk2(f, f), m2 = codec::pk2(-mm, -mm);
   uint64_t a[2] = {0ull, 0ull};
-  uint32_t any[2] = {0u, 0u};
+  tc_wait_ld();
+  if (want_exact) {  // formed once more rather than summed beside every other call's
 #pragma unroll
-  for (int j = 0; j < kHalf / 2; ++j) {
+    for (int j = 0; j < 32; ++j) exact += ex2(fmaf(__uint_as_float(s[j]), f, -mm));
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
     const uint64_t y = codec::fma2(codec::pk2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), f2, m2);
     const uint32_t h0 = __float_as_uint(ex2(codec::pk_lo(y))) & 0xffff0000u;
     const uint32_t h1 = __float_as_uint(ex2(codec::pk_hi(y))) & 0xffff0000u;
-    w[j] = __byte_perm(h0, h1, 0x7632);
-    any[j & 1] |= w[j];
+    w[o + j] = __byte_perm(h0, h1, 0x7632);
+    bits |= w[o + j];
     a[j & 1] = codec::add2(a[j & 1], codec::pk2(__uint_as_float(h0), __uint_as_float(h1)));
   }
   const uint64_t t = codec::add2(a[0], a[1]);
-  sum = codec::pk_lo(t) + codec::pk_hi(t);
-  bits = any[0] | any[1];
+  sum += codec::pk_lo(t) + codec::pk_hi(t);
+}
+// the largest of 32 logits of this thread's row
+__device__ __forceinline__ float max32(uint32_t ts) {
+  uint32_t s[32];
+  tc_ld32(ts, s, 0);
+  tc_wait_ld();
+  float mx = __uint_as_float(s[0]);
+#pragma unroll
+  for (int j = 1; j < 31; j += 2) mx = max3(mx, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+  return fmaxf(mx, __uint_as_float(s[31]));
 }
 
 // The sum of channel `ch` over the new tokens that row i sees and whose value there is not
@@ -570,11 +551,11 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   const int lane_parts = p.splits / gridDim.y;  // 2 when the lanes end as two splits
   const size_t part_rows = static_cast<size_t>(p.span.n) * p.G;
   // this softmax thread's query row
-  const int wl = (warp >> 2) & 1;  // lane of the softmax warp
+  const int wl = (warp >> 3) & 1, wh = (warp >> 2) & 1;  // lane and half of the softmax warp
   const int x = xb + (PAIR ? wl * kBlock : 0) + (warp & 3) * 32 + lane;
 
   if (tiles == 0) {  // nothing to read: the rows' share of this split is empty
-    if (warp < 8 && x < rows && (PAIR || wl < lane_parts)) {
+    if (warp < kDecodeWarp && wh == 0 && x < rows && (PAIR || wl < lane_parts)) {
       if (p.splits > 1) {
         p.part_ml[(static_cast<size_t>(unit) * p.splits + blockIdx.y * lane_parts + (PAIR ? 0 : wl)) * part_rows + x] =
             make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
@@ -603,6 +584,8 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   auto s_full = [&](int l, int h) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + 2 * l + h); };
   auto p_full = [&](int l, int h) { return bars + 8 * (5 + 2 * kKStages + 2 * VS + 2 * l + h); };
   auto o_done = [&](int l, int h) { return bars + 8 * (9 + 2 * kKStages + 2 * VS + 2 * l + h); };
+  // of a half's warp: its step has settled on m
+  auto settled = [&](int l, int q, int h) { return bars + 8 * (13 + 2 * kKStages + 2 * VS + 8 * l + 2 * q + h); };
 
   // tiles of lane l: PAIR all of them (when the lane has rows), else those of its parity
   const int lanes_on = PAIR ? (xb + kBlock < rows ? 2 : 1) : (tiles > 1 ? 2 : 1);
@@ -625,6 +608,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         mbar_init(s_full(l, h), 1);
         mbar_init(p_full(l, h), max(1, min(4, (r0 + 31) / 32)));  // warps that have rows
         mbar_init(o_done(l, h), 1);
+        for (int q = 0; q < 4; ++q) mbar_init(settled(l, q, h), 1);
       }
     }
     misc[1] = 0u;
@@ -641,9 +625,6 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
   bool ok = true;
 
-  // Registers move from the other warps to the softmax warps, a warpgroup at a time.
-  if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kTmaWarp) {
     if (lane == 0) {
       const int nq = PAIR ? lanes_on : 1;
@@ -671,7 +652,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       }
       if (!mbar_wait(q_full, 0)) ok = false;
     }
-  } else if (warp < kTmaWarp) {
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // The halves of a lane's tile take turns: while the exponentials of one run, the other's
     // readout and next logits do.
     const int l = warp - kMmaWarp, n = lane_tiles(l);
@@ -724,9 +705,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     // the products are done before TMEM is given back
     if (n > 0 && ok) wait(o_done(l, 1), n - 1);
     __syncwarp();
-  }
-  } else if (warp >= kDecodeWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
+  } else if (warp >= kDecodeWarp && warp < kMmaWarp) {
     const int tok = (tid - kDecodeWarp * 32) & (kTile - 1), half = (warp - kDecodeWarp) >> 2;
     float* red = reinterpret_cast<float*>(misc + 4);  // [2][8] warp maxima
     constexpr int HG = NG / 2;  // groups of this half
@@ -829,9 +808,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       }
       cur = nxt;
     }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-  if (xb + (PAIR ? wl * kBlock : 0) + (warp & 3) * 32 < rows && wl < lanes_on) {
+  } else if (warp < kDecodeWarp && xb + (PAIR ? wl * kBlock : 0) + (warp & 3) * 32 < rows && wl < lanes_on) {
     // ---- softmax and epilogue of this warp's 32 query rows
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + 128 * wl + lane_off, to = tmem + 256 + 128 * wl + lane_off;
@@ -839,72 +816,77 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     const float fq = t.qf[static_cast<size_t>(unit) * t.blocks * kBlock + x];
     const uint32_t* words = t.words ? t.words + (static_cast<size_t>(b) * p.span.n + i) * t.wpr : nullptr;
     const bool want_lse = p.lse != nullptr;
-    RowState st{-INFINITY, 0.0f, 0.0f};
-    const int nk = lane_tiles(wl);
-    // One half-tile at a time; the next one's logits are on their way while this one's
-    // weights are written.
-    uint32_t s[kHalf];
-    float f = 0.0f;
-    const int tail_at = min(P, t_hi) >= t_lo ? (min(P, t_hi) - t_lo) / kTile : 0;  // tiles from here on hold new tokens or end the sequence
+    const int nk = lane_tiles(wl), quad = warp & 3;
+    // tiles from here on hold new tokens or end the sequence
+    const int tail_at = min(P, t_hi) >= t_lo ? (min(P, t_hi) - t_lo) / kTile : 0;
+    float* m_s = reinterpret_cast<float*>(sm + Ly::kMax) + wl * kBlock + quad * 32 + lane;
+    const uint32_t sa = ts + kHalf * wh;
+    // The two halves of a tile are two warps' work, on one m (they share the accumulator).
+    // Each forms its weights with the m it knows, then takes its turn (half 0 of a tile, half
+    // 1, half 0 of the next: the order of the readouts anyway) to learn of the other's m and
+    // to raise it.
+    float m = -INFINITY, l = 0.0f, lx = 0.0f;
 #pragma unroll 1
-    for (int y = -1; y < 2 * nk && ok; ++y) {  // step y: half y & 1 of the lane's tile y / 2
-      const int h = y & 1;
-      if (y >= 0) {
-        tc_wait_ld();
-        uint32_t w[kHalf / 2], bits;
-        float sum;
-        weights(s, f, st.m, w, sum, bits);
-        // a weight of 2 or more (or not a number), or no m yet: find it, and the weights again
-        if (__any_sync(kAll, (bits & 0x40004000u) != 0u || y == 0)) {
-          float mx = __uint_as_float(s[0]);
-#pragma unroll
-          for (int j = 1; j < kHalf - 1; j += 2) mx = max3(mx, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-          const float top = fmaxf(mx, __uint_as_float(s[kHalf - 1])) * f;
+    for (int k = 0; k < nk; ++k) {
+      const int tile = tile_of(wl, k);
+      const float* col = scale_s + (tile % kRing) * kTile;
+      if (!mbar_wait(s_full(wl, wh), k & 1)) { ok = false; break; }
+      tc_fence_after();
+      float f = fmaxf(fq * col[0], 1e-37f);
+      if (tile >= tail_at) {
+        f = fmaxf(fq, 1e-37f);
+        mask_half(sa, words, t.wpr, i, t_lo + tile * kTile + kHalf * wh - P, col + kHalf * wh);
+      }
+      uint32_t w[kHalf / 2], bits = 0u;
+      float sum = 0.0f, sumx = 0.0f;
+      weights32(sa, f, m, w, 0, sum, bits, want_lse, sumx);
+      weights32(sa + 32, f, m, w, 16, sum, bits, want_lse, sumx);
+      const bool first = k == 0 && wh == 0;
+      if (!first && !mbar_wait(settled(wl, quad, 1 - wh), (wh ? k : k - 1) & 1)) { ok = false; break; }
+      const float known = first ? -INFINITY : *m_s;
+      // another m than these weights', a weight of 2 or more (or not a number), or no m yet
+      if (__any_sync(kAll, known != m || (bits & 0x40004000u) != 0u || m == -INFINITY)) {
+        const float top = fmaxf(max32(sa), max32(sa + 32)) * f;
+        const float m2 = top > known ? top + kSlack : known;
+        if (!first && __any_sync(kAll, m2 > known)) {
           // the accumulator rests once the half before this one is read out
-          if (y > 0 && !mbar_wait(o_done(wl, 1 - h), ((y - 1) >> 1) & 1)) ok = false;
+          if (!mbar_wait(o_done(wl, 1 - wh), (wh ? k : k - 1) & 1)) ok = false;
           tc_fence_after();
-          st = raise_max<D>(st, top > st.m ? top + kSlack : st.m, to, y > 0);
-          weights(s, f, st.m, w, sum, bits);
+          scale_output<D>(to, known == -INFINITY ? 0.0f : ex2(known - m2));
         }
-        st.l += sum;
-        if (want_lse) {  // the unrounded weights once more, rather than their sums beside every other call's
-          const float mm = st.m == -INFINITY ? 0.0f : st.m;
-#pragma unroll
-          for (int j = 0; j < kHalf; ++j) st.lx += ex2(fmaf(__uint_as_float(s[j]), f, -mm));
-        }
-        tc_st16(ts + kHalf * h, w, 0);
-        tc_st16(ts + kHalf * h + 16, w, 16);
+        *m_s = m2;
+        const float a = m == -INFINITY ? 0.0f : ex2(m - m2);
+        l *= a;
+        lx *= a;
+        m = m2;
+        sum = sumx = 0.0f;
+        weights32(sa, f, m, w, 0, sum, bits, want_lse, sumx);
+        weights32(sa + 32, f, m, w, 16, sum, bits, want_lse, sumx);
       }
-      auto hand_over = [&]() {
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(wl, h));
-      };
-      bool handed = y < 0;
-      if (y + 1 < 2 * nk) {
-        const uint32_t bar = s_full(wl, 1 - h), parity = ((y + 1) >> 1) & 1;
-        if (!__all_sync(kAll, mbar_test(bar, parity))) {  // not there yet: this one's weights first
-          if (!handed) hand_over();
-          handed = true;
-          if (!mbar_wait(bar, parity)) ok = false;
-        }
-        const int tile = tile_of(wl, (y + 1) >> 1);
-        const float* col = scale_s + (tile % kRing) * kTile;
-        const uint32_t sa = ts + kHalf * (1 - h);
-        tc_fence_after();
-        f = fmaxf(fq * col[0], 1e-37f);
-        if (tile >= tail_at) {
-          f = fmaxf(fq, 1e-37f);
-          mask_half(sa, words, t.wpr, i, t_lo + tile * kTile + kHalf * (1 - h) - P, col + kHalf * (1 - h));
-        }
-        tc_ld32(sa, s, 0);
-        tc_ld32(sa + 32, s, 32);
-      }
-      if (!handed) hand_over();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(settled(wl, quad, wh));
+      tc_st16(sa, w, 0);
+      tc_st16(sa + 16, w, 16);
+      l += sum;
+      lx += sumx;
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(wl, wh));
     }
-    const float m = st.m, l = st.l, lx = st.lx;
-    if (ok && nk > 0 && !mbar_wait(o_done(wl, 1), (nk - 1) & 1)) ok = false;
+    if (ok && wh == 0 && !mbar_wait(settled(wl, quad, 1), (nk - 1) & 1)) ok = false;
+    if (ok) {  // half 1's last m is the row's
+      const float m2 = *m_s, a = m == -INFINITY ? 0.0f : ex2(m - m2);
+      l *= a;
+      lx *= a;
+      m = m2;
+    }
+    float2* sums = reinterpret_cast<float2*>(sm + Ly::kSums) + 2 * wl * kBlock + quad * 32 + lane;
+    sums[wh * kBlock] = make_float2(l, lx);
+    asm volatile("bar.sync %0, 64;" ::"r"(2 + 4 * wl + quad) : "memory");
+    l += sums[(1 - wh) * kBlock].x;
+    lx += sums[(1 - wh) * kBlock].y;
+    if (ok && !mbar_wait(o_done(wl, 1), (nk - 1) & 1)) ok = false;
     tc_fence_after();
     if (ok) {
       const bool bad = *reinterpret_cast<volatile uint32_t*>(misc + 1) != 0u;
@@ -916,7 +898,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       const float inv = !direct ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
       if (bad) {  // rare: one column at a time, in TMEM
 #pragma unroll 1
-        for (int c = 0; c < D; ++c) {
+        for (int c = wh * (D / 2); c < (wh + 1) * (D / 2); ++c) {
           const float add = bad_values<V2, PAIR>(p, words, t.wpr, i, b, kv, max(P, t_lo), t_lo, t_hi, P, wl,
                                                  V2 ? channel_at(c) : c);
           uint32_t w;
@@ -928,7 +910,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         tc_wait_st();
       }
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = wh * (D / 64); c < (wh + 1) * (D / 64); ++c) {  // half the channels each
         uint32_t w[32];
         tc_ld32(to + 32 * c, w, 0);
         tc_wait_ld();
@@ -948,16 +930,15 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
           }
         }
       }
-      if (x < rows) {
+      if (wh == 0 && x < rows) {
         if (!direct) p.part_ml[pr] = make_float4(m * dc::kLn2, l, lx, 0.0f);
         else if (want_lse) p.lse[orow * p.Hq + h] = l == 0.0f ? -INFINITY : m * dc::kLn2 + logf(lx);
       }
     }
-  } else if (x < rows && !PAIR && wl < lane_parts) {
+  } else if (warp < kDecodeWarp && wh == 0 && x < rows && !PAIR && wl < lane_parts) {
     // the lane without a tile: its split is empty
     p.part_ml[(static_cast<size_t>(unit) * p.splits + blockIdx.y * lane_parts + wl) * part_rows + x] =
         make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-  }
   }
 
   if (!ok) atomicOr(p.err, kDevErrWaitTimeout);
