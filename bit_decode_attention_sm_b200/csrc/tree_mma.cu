@@ -19,11 +19,11 @@
 //     transpose within each 16, and the queries are stored in that order too.  2-bit values
 //     the same way in bf16.
 //   1 TMA warp       dense bf16 values, 64 tokens x 64 channels a box
-//   2 MMA warps      one per lane (below): logits into TMEM, readout from the weights there
+//   2 MMA threads    one per lane (below): logits into TMEM, readout from the weights there
 //   2 x 2 x 4 softmax warps: two "lanes", in each one thread per query row and half a tile.  PAIR (more than 128 rows):
 //     the lanes hold two row blocks over the same tiles, so each decoded tile serves 256
 //     rows; else they take alternate tiles of the one block and end as two splits.
-// The running maximum is kept with a slack of 2^40 (kSlack): one pass over the logits and no
+// The running maximum is kept with a slack of 2^60 (kSlack): one pass over the logits and no
 // search for the maximum in it, and the output accumulator in TMEM is rescaled only when a
 // weight reaches 2, which is rare (with a slack of 2^8 it was a third of the steps in peaked
 // attention).  Weights are
@@ -55,8 +55,8 @@ constexpr int kRing = 8;            // tiles whose key scales are kept (more tha
 // A row's weights are 2^(logit - m) with m at least the largest logit so far and, when it is
 // set, kSlack above it: the check that a step stays below 2 is then one bit of the weights,
 // and m is seldom set again.  Weights, sums and accumulators all have the 8-bit exponent of
-// fp32, so the offset costs no precision (a weight 2^-86 of the largest is still normal).
-constexpr float kSlack = 40.0f;
+// fp32, so the offset costs no precision (a weight 2^-66 of the largest is still normal).
+constexpr float kSlack = 60.0f;
 constexpr uint32_t kAll = 0xffffffffu;
 
 // bytes of 128 operand rows: d channels in 64-channel blocks (128-byte rows, 128-byte
@@ -66,33 +66,25 @@ __host__ __device__ constexpr int operand_bytes(int d, int r) { return kTile * (
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// The next three are executed by the whole warp and take effect for the thread with `one`
-// set: their operands are then the same in every lane, and need no moves out of per-thread
-// registers between one product and the next.
-__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t one) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
-      "r"(one)
-      : "memory");
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// descriptors as their two words
+// descriptors as their two words: the high ones are constants, the low ones one addition apart
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
-                                          uint32_t idesc, bool acc, uint32_t one) {
+                                          uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 da, db;\n setp.ne.u32 p, %6, 0;\n setp.ne.u32 q, %7, 0;\n"
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.u32 p, %6, 0;\n"
       " mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(one)
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc))
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, bool acc,
-                                          uint32_t one) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 db;\n setp.ne.u32 p, %5, 0;\n setp.ne.u32 q, %6, 0;\n"
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.u32 p, %5, 0;\n"
       " mov.b64 db, {%2, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(one)
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc))
       : "memory");
 }
 template <int N>
@@ -115,6 +107,16 @@ __device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(a));
+}
+__device__ __forceinline__ void tc_ld4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+__device__ __forceinline__ void tc_st4(uint32_t a, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0,%1,%2,%3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(a)
+               : "memory");
 }
 template <int N>
 __device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&v)[N], int o) {
@@ -150,6 +152,20 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
     for (int k = 0; k < 256; ++k)
       if (mbar_try(bar, parity)) return true;
+  } while (clock64() - start < dc::kWaitCycles);
+  return false;
+}
+// The same for the warps that wait long and are many: a short sleep between the tries leaves
+// the issue slots to the others.
+__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity) {
+  if (mbar_try(bar, parity)) return true;
+  const long long start = clock64();
+  do {
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k) {
+      __nanosleep(32);
+      if (mbar_try(bar, parity)) return true;
+    }
   } while (clock64() - start < dc::kWaitCycles);
   return false;
 }
@@ -342,8 +358,9 @@ struct Layout {
   static constexpr int kScale = kV + kVStages * kVTile;  // [kRing][kTile] floats
   static constexpr int kMax = kScale + kRing * kTile * 4;  // [2 lanes][kBlock] floats: m of each row
   static constexpr int kSums = kMax + 2 * kBlock * 4;      // [2 lanes][2 halves][kBlock] float2: sums of each row
-  static constexpr int kBars = kSums + 4 * kBlock * 8;
-  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 12 + 16;
+  static constexpr int kTurn = kSums + 4 * kBlock * 8;     // [2 lanes][4 quadrants][2 halves]: steps settled on an m
+  static constexpr int kBars = kTurn + 16 * 4;
+  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 12;
   static constexpr int kMisc = (kBars + 8 * kNumBars + 15) & ~15;  // tmem base, bad-value flag, 2 x 8 maxima
   static constexpr int kBytes = kMisc + 128 + 1024;    // and room for the alignment
 };
@@ -440,17 +457,59 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int wpr, int 
   return __funnelshift_r(mask_word(row, wpr, i, k), mask_word(row, wpr, i, k + 1), a & 31);
 }
 
+// kSlack above the largest of 32 logits (times f), or -inf
+__device__ __forceinline__ float row_max(const uint32_t (&u)[32], float f) {
+  float mx = __uint_as_float(u[0]);
+#pragma unroll
+  for (int j = 1; j < 31; j += 2) mx = max3(mx, __uint_as_float(u[j]), __uint_as_float(u[j + 1]));
+  return fmaxf(mx, __uint_as_float(u[31])) * f + kSlack;
+}
+
+// 32 logits of this thread's row (times f: log2 units) to weights relative to 2^m, two to a
+// word; their sum, and all their bits
+__device__ __forceinline__ void weights32(const uint32_t (&u)[32], float f, float m, uint32_t (&w)[16], float& sum,
+                                          uint32_t& bits) {
+  const float mm = m == -INFINITY ? 0.0f : m;
+  const uint64_t f2 = codec::pk2(f, f), m2 = codec::pk2(-mm, -mm);
+  uint64_t a[2] = {0ull, 0ull};
+  bits = 0u;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const uint64_t y = codec::fma2(codec::pk2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])), f2, m2);
+    const uint32_t h0 = __float_as_uint(ex2(codec::pk_lo(y))) & 0xffff0000u;
+    const uint32_t h1 = __float_as_uint(ex2(codec::pk_hi(y))) & 0xffff0000u;
+    w[j] = __byte_perm(h0, h1, 0x7632);
+    bits |= w[j];
+    a[j & 1] = codec::add2(a[j & 1], codec::pk2(__uint_as_float(h0), __uint_as_float(h1)));
+  }
+  const uint64_t t = codec::add2(a[0], a[1]);
+  sum = codec::pk_lo(t) + codec::pk_hi(t);
+}
+
+// Wait until the other half's warp has settled `steps` steps (a word in shared memory: a
+// load, where a barrier would cost several times that); false after about 2 s.
+__device__ __forceinline__ bool wait_turn(const volatile int* turn, int steps) {
+  if (*turn >= steps) return true;
+  const long long start = clock64();
+#pragma unroll 1
+  while (*turn < steps) {
+    __nanosleep(32);
+    if (clock64() - start > dc::kWaitCycles) return false;
+  }
+  return true;
+}
+
 // The accumulator of this thread's row times a.
 template <int D>
 __device__ __forceinline__ void scale_output(uint32_t to, float a) {
 #pragma unroll 1
-  for (int o = 0; o < D; o += 16) {
-    uint32_t w[16];
-    tc_ld16(to + o, w);
+  for (int o = 0; o < D; o += 4) {
+    uint32_t w[4];
+    tc_ld4(to + o, w);
     tc_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * a);
-    tc_st16(to + o, w, 0);
+    for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * a);
+    tc_st4(to + o, w);
   }
   tc_wait_st();
 }
@@ -474,42 +533,26 @@ __device__ __forceinline__ void mask_half(uint32_t ts, const uint32_t* row, int 
   tc_wait_st();
 }
 
-// 32 logits of this thread's row (times f: log2 units) to weights relative to 2^m, two to a
-// word (w + o); their sum, all their bits, and (exact) the sum of the unrounded ones.
-template <int N>
-__device__ __forceinline__ void weights32(uint32_t ts, float f, float m, uint32_t (&w)[N], int o, float& sum,
-                                          uint32_t& bits, bool want_exact, float& exact) {
-  uint32_t s[32];
-  tc_ld32(ts, s, 0);
-  const float mm = m == -INFINITY ? 0.0f : m;
-  const uint64_t f2 = codec::pk2(f, f), m2 = codec::pk2(-mm, -mm);
-  uint64_t a[2] = {0ull, 0ull};
-  tc_wait_ld();
-  if (want_exact) {  // formed once more rather than summed beside every other call's
+// Weights two to a word, in TMEM columns [ts, ts + n): times a, truncated again; the change
+// that truncation makes to their sum.
+__device__ __forceinline__ float scale_weights(uint32_t ts, int n, float a) {
+  float change = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < n; c += 4) {
+    uint32_t w[4];
+    tc_ld4(ts + c, w);
+    tc_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 32; ++j) exact += ex2(fmaf(__uint_as_float(s[j]), f, -mm));
+    for (int j = 0; j < 4; ++j) {
+      const float e0 = __uint_as_float(w[j] << 16) * a, e1 = __uint_as_float(w[j] & 0xffff0000u) * a;
+      const uint32_t h0 = __float_as_uint(e0) & 0xffff0000u, h1 = __float_as_uint(e1) & 0xffff0000u;
+      change += (__uint_as_float(h0) - e0) + (__uint_as_float(h1) - e1);
+      w[j] = (h0 >> 16) | h1;
+    }
+    tc_st4(ts + c, w);
   }
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint64_t y = codec::fma2(codec::pk2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), f2, m2);
-    const uint32_t h0 = __float_as_uint(ex2(codec::pk_lo(y))) & 0xffff0000u;
-    const uint32_t h1 = __float_as_uint(ex2(codec::pk_hi(y))) & 0xffff0000u;
-    w[o + j] = __byte_perm(h0, h1, 0x7632);
-    bits |= w[o + j];
-    a[j & 1] = codec::add2(a[j & 1], codec::pk2(__uint_as_float(h0), __uint_as_float(h1)));
-  }
-  const uint64_t t = codec::add2(a[0], a[1]);
-  sum += codec::pk_lo(t) + codec::pk_hi(t);
-}
-// the largest of 32 logits of this thread's row
-__device__ __forceinline__ float max32(uint32_t ts) {
-  uint32_t s[32];
-  tc_ld32(ts, s, 0);
-  tc_wait_ld();
-  float mx = __uint_as_float(s[0]);
-#pragma unroll
-  for (int j = 1; j < 31; j += 2) mx = max3(mx, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-  return fmaxf(mx, __uint_as_float(s[31]));
+  tc_wait_st();
+  return change;
 }
 
 // The sum of channel `ch` over the new tokens that row i sees and whose value there is not
@@ -584,14 +627,12 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   auto s_full = [&](int l, int h) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + 2 * l + h); };
   auto p_full = [&](int l, int h) { return bars + 8 * (5 + 2 * kKStages + 2 * VS + 2 * l + h); };
   auto o_done = [&](int l, int h) { return bars + 8 * (9 + 2 * kKStages + 2 * VS + 2 * l + h); };
-  // of a half's warp: its step has settled on m
-  auto settled = [&](int l, int q, int h) { return bars + 8 * (13 + 2 * kKStages + 2 * VS + 8 * l + 2 * q + h); };
-
   // tiles of lane l: PAIR all of them (when the lane has rows), else those of its parity
   const int lanes_on = PAIR ? (xb + kBlock < rows ? 2 : 1) : (tiles > 1 ? 2 : 1);
   auto lane_tiles = [&](int l) { return l >= lanes_on ? 0 : PAIR ? tiles : (tiles - l + 1) / 2; };
   auto tile_of = [&](int l, int k) { return PAIR ? k : 2 * k + l; };
 
+  if (tid < 16) reinterpret_cast<int*>(sm + Ly::kTurn)[tid] = 0;
   if (tid == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < kKStages; ++s) {
@@ -608,7 +649,6 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         mbar_init(s_full(l, h), 1);
         mbar_init(p_full(l, h), max(1, min(4, (r0 + 31) / 32)));  // warps that have rows
         mbar_init(o_done(l, h), 1);
-        for (int q = 0; q < 4; ++q) mbar_init(settled(l, q, h), 1);
       }
     }
     misc[1] = 0u;
@@ -635,7 +675,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         int issued = 0;
         for (int k = 0; k < tiles && ok; ++k) {
           const int s = k % VS;
-          if (k >= VS && !mbar_wait(v_empty(s), ((k / VS) - 1) & 1)) { ok = false; break; }
+          if (k >= VS && !mbar_wait_idle(v_empty(s), ((k / VS) - 1) & 1)) { ok = false; break; }
           const int t0 = t_lo + k * kTile;
           const int halves = t0 + 64 < t_hi ? 2 : 1;
           mbar_expect_tx(v_full(s), halves * 64 * D * 2);
@@ -653,57 +693,54 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       if (!mbar_wait(q_full, 0)) ok = false;
     }
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-    // The halves of a lane's tile take turns: while the exponentials of one run, the other's
-    // readout and next logits do.
+    // One thread per lane.  Step -1: the logits of tile 0; step k: the readout of tile k, each
+    // half followed by its logits of tile k + 1, which overwrite the weights it read.
     const int l = warp - kMmaWarp, n = lane_tiles(l);
-    constexpr uint32_t kLogit = mma_desc(0, 0, kTile / 2);  // fp16, both operands K-major
-    constexpr uint32_t kRead = mma_desc(1, 1, D);           // bf16, values channel-major
-    constexpr uint32_t kSwz = desc_hi(1024, 2), kFlat = desc_hi(128, 0);
-    constexpr uint32_t kSide = D / 64 * (kTile * 128);  // the side entries within an operand
-    const uint32_t one = lane == 0;
-    const uint32_t qa = base + Ly::kQ + (PAIR ? l * Ly::kOperand : 0);
-    const uint32_t q_lo = desc_lo(qa, 16), qs_lo = desc_lo(qa + kSide, kTile * 16);
-    const uint32_t k_lo = desc_lo(base + Ly::kK, 16), ks_lo = desc_lo(base + Ly::kK + kSide, kTile * 16);
-    const uint32_t v_lo = desc_lo(base + Ly::kV, kTile * 128);
-    auto wait = [&](uint32_t bar, int phase) {
-      ok = __all_sync(kAll, ok && mbar_wait(bar, phase & 1));
-      return ok;
-    };
-    // step -1: logits of tile 0; step k: readout of tile k, each half followed by its logits
-    // of tile k + 1, which overwrite the weights it read
-    if (n > 0) wait(q_full, 0);
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t kLogit = mma_desc(0, 0, kTile / 2);  // fp16, both operands K-major
+      constexpr uint32_t kRead = mma_desc(1, 1, D);           // bf16, values channel-major
+      constexpr uint32_t kSwz = desc_hi(1024, 2), kFlat = desc_hi(128, 0);
+      constexpr uint32_t kSide = D / 64 * (kTile * 128);  // the side entries within an operand
+      const uint32_t qa = base + Ly::kQ + (PAIR ? l * Ly::kOperand : 0);
+      const uint32_t q_lo = desc_lo(qa, 16), qs_lo = desc_lo(qa + kSide, kTile * 16);
+      const uint32_t k_lo = desc_lo(base + Ly::kK, 16), ks_lo = desc_lo(base + Ly::kK + kSide, kTile * 16);
+      const uint32_t v_lo = desc_lo(base + Ly::kV, kTile * 128);
+      ok = mbar_wait(q_full, 0);
 #pragma unroll 1
-    for (int y = -2; y < 2 * n && ok; ++y) {
-      const int k = y >> 1, h = y & 1;
-      if (k >= 0) {
-        const int tile = tile_of(l, k), s = tile % VS;
-        if (!wait(p_full(l, h), k) || !wait(v_full(s), tile / VS)) break;
-        tc_fence_after();
-        const uint32_t va = v_lo + ((s * Ly::kVTile + 8192 * h) >> 4), w = tmem + 128 * l + 64 * h;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          tc_mma_ts(tmem + 256 + 128 * l, w + 8 * e, va + (2048 >> 4) * e, kSwz, kRead, y > 0 || e > 0, one);
-        tc_commit(o_done(l, h), one);
-        if (h == 1) tc_commit(v_empty(s), one);
-      }
-      if (k + 1 < n) {
-        const int tile = tile_of(l, k + 1), s = tile % kKStages;
-        if ((k >= 0 && !wait(o_done(l, h), k)) || !wait(k_full(s), tile / kKStages)) break;
-        tc_fence_after();
-        const uint32_t ka = (s * Ly::kOperand + 8192 * h) >> 4, d = tmem + 128 * l + 64 * h;
-#pragma unroll
-        for (int e = 0; e < D / 16; ++e) {
-          const uint32_t off = ((e >> 2) * (kTile * 128) + 32 * (e & 3)) >> 4;
-          tc_mma_ss(d, q_lo + off, kSwz, k_lo + ka + off, kSwz, kLogit, e > 0, one);
+      for (int y = -2; y < 2 * n && ok; ++y) {
+        const int k = y >> 1, h = y & 1;
+        if (k >= 0) {
+          const int tile = tile_of(l, k), s = tile % VS;
+          if (h == 0 && !mbar_wait(v_full(s), (tile / VS) & 1)) { ok = false; break; }
+          if (!mbar_wait(p_full(l, h), k & 1)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t va = v_lo + ((s * Ly::kVTile + 8192 * h) >> 4), w = tmem + 128 * l + 64 * h;
+#pragma unroll 1
+          for (int e = 0; e < 4; ++e)
+            tc_mma_ts(tmem + 256 + 128 * l, w + 8 * e, va + (2048 >> 4) * e, kSwz, kRead, y > 0 || e > 0);
+          tc_commit(o_done(l, h));
+          if (h == 1) tc_commit(v_empty(s));
         }
-        if constexpr (R > 0)
-          tc_mma_ss(d, qs_lo, kFlat, ks_lo + ((s * Ly::kOperand + 1024 * h) >> 4), kFlat, kLogit, true, one);
-        tc_commit(s_full(l, h), one);
-        if (h == 1) tc_commit(k_empty(s), one);
+        if (k + 1 < n) {
+          const int tile = tile_of(l, k + 1), s = tile % kKStages;
+          if (h == 0 && !mbar_wait(k_full(s), (tile / kKStages) & 1)) { ok = false; break; }
+          if (k >= 0 && !mbar_wait(o_done(l, h), k & 1)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t ka = (s * Ly::kOperand + 8192 * h) >> 4, d = tmem + 128 * l + 64 * h;
+#pragma unroll 1
+          for (int e = 0; e < D / 16; ++e) {
+            const uint32_t off = ((e >> 2) * (kTile * 128) + 32 * (e & 3)) >> 4;
+            tc_mma_ss(d, q_lo + off, kSwz, k_lo + ka + off, kSwz, kLogit, e > 0);
+          }
+          if constexpr (R > 0)
+            tc_mma_ss(d, qs_lo, kFlat, ks_lo + ((s * Ly::kOperand + 1024 * h) >> 4), kFlat, kLogit, true);
+          tc_commit(s_full(l, h));
+          if (h == 1) tc_commit(k_empty(s));
+        }
       }
+      // the products are done before TMEM is given back
+      if (ok && !mbar_wait(o_done(l, 1), (n - 1) & 1)) ok = false;
     }
-    // the products are done before TMEM is given back
-    if (n > 0 && ok) wait(o_done(l, 1), n - 1);
     __syncwarp();
   } else if (warp >= kDecodeWarp && warp < kMmaWarp) {
     const int tok = (tid - kDecodeWarp * 32) & (kTile - 1), half = (warp - kDecodeWarp) >> 2;
@@ -727,7 +764,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       const uint32_t wm = __reduce_max_sync(kAll, __float_as_uint(mx));
       if (lane == 0) red[(k & 1) * 8 + warp - kDecodeWarp] = __uint_as_float(wm);
       // one warp waits for the stage, the others for the barrier that they meet at anyway
-      if (warp == kDecodeWarp && k >= kKStages && ok && !mbar_wait(k_empty(s), ((k / kKStages) - 1) & 1)) ok = false;
+      if (warp == kDecodeWarp && k >= kKStages && ok && !mbar_wait_idle(k_empty(s), ((k / kKStages) - 1) & 1)) ok = false;
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (!tail) {  // one power of two per tile; else one per token: an unseen new token's size touches no other
         const float4 m4 = *reinterpret_cast<const float4*>(red + (k & 1) * 8);  // half 0's four have them all
@@ -819,7 +856,8 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     const int nk = lane_tiles(wl), quad = warp & 3;
     // tiles from here on hold new tokens or end the sequence
     const int tail_at = min(P, t_hi) >= t_lo ? (min(P, t_hi) - t_lo) / kTile : 0;
-    float* m_s = reinterpret_cast<float*>(sm + Ly::kMax) + wl * kBlock + quad * 32 + lane;
+    volatile float* m_s = reinterpret_cast<volatile float*>(sm + Ly::kMax) + wl * kBlock + quad * 32 + lane;
+    volatile int* turn = reinterpret_cast<volatile int*>(sm + Ly::kTurn) + 8 * wl + 2 * quad;
     const uint32_t sa = ts + kHalf * wh;
     // The two halves of a tile are two warps' work, on one m (they share the accumulator).
     // Each forms its weights with the m it knows, then takes its turn (half 0 of a tile, half
@@ -830,53 +868,71 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     for (int k = 0; k < nk; ++k) {
       const int tile = tile_of(wl, k);
       const float* col = scale_s + (tile % kRing) * kTile;
-      if (!mbar_wait(s_full(wl, wh), k & 1)) { ok = false; break; }
+      if (!mbar_wait_idle(s_full(wl, wh), k & 1)) { ok = false; break; }
       tc_fence_after();
       float f = fmaxf(fq * col[0], 1e-37f);
       if (tile >= tail_at) {
         f = fmaxf(fq, 1e-37f);
         mask_half(sa, words, t.wpr, i, t_lo + tile * kTile + kHalf * wh - P, col + kHalf * wh);
       }
-      uint32_t w[kHalf / 2], bits = 0u;
-      float sum = 0.0f, sumx = 0.0f;
-      weights32(sa, f, m, w, 0, sum, bits, want_lse, sumx);
-      weights32(sa + 32, f, m, w, 16, sum, bits, want_lse, sumx);
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {  // 32 tokens each, by one piece of code: the roles share the instruction cache
+        uint32_t u[32];
+        tc_ld32(sa + 32 * c, u, 0);
+        tc_wait_ld();
+        if (!(m > -INFINITY)) m = row_max(u, f);  // (a row that has seen nothing stays at -inf)
+        uint32_t w[16], bits;
+        float sum;
+        weights32(u, f, m, w, sum, bits);
+        if (__any_sync(kAll, (bits & 0x40004000u) != 0u)) {  // a weight of 2 or more, or not a number
+          const float m2 = fmaxf(m, row_max(u, f)), a = m == m2 ? 1.0f : ex2(m - m2);
+          l *= a;
+          lx *= a;
+          if (c) l += scale_weights(sa, 16, a);
+          m = m2;
+          weights32(u, f, m, w, sum, bits);
+        }
+        l += sum;
+        if (want_lse) {  // formed once more rather than summed beside every other call's
+          const float mm = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) lx += ex2(fmaf(__uint_as_float(u[j]), f, -mm));
+        }
+        tc_st16(sa + 16 * c, w, 0);
+      }
+      // this half's turn: the two halves agree on the larger m
+      if (!wait_turn(turn + 1 - wh, k + wh)) { ok = false; break; }
       const bool first = k == 0 && wh == 0;
-      if (!first && !mbar_wait(settled(wl, quad, 1 - wh), (wh ? k : k - 1) & 1)) { ok = false; break; }
-      const float known = first ? -INFINITY : *m_s;
-      // another m than these weights', a weight of 2 or more (or not a number), or no m yet
-      if (__any_sync(kAll, known != m || (bits & 0x40004000u) != 0u || m == -INFINITY)) {
-        const float top = fmaxf(max32(sa), max32(sa + 32)) * f;
-        const float m2 = top > known ? top + kSlack : known;
+      const float known = first ? m : *m_s;
+      if (__any_sync(kAll, known != m)) {
+        const float m2 = fmaxf(known, m);
+        if (__any_sync(kAll, m2 > m)) {
+          const float a = m == -INFINITY ? 0.0f : ex2(m - m2);
+          l *= a;
+          lx *= a;
+          tc_wait_st();
+          l += scale_weights(sa, 32, a);
+        }
         if (!first && __any_sync(kAll, m2 > known)) {
           // the accumulator rests once the half before this one is read out
           if (!mbar_wait(o_done(wl, 1 - wh), (wh ? k : k - 1) & 1)) ok = false;
           tc_fence_after();
           scale_output<D>(to, known == -INFINITY ? 0.0f : ex2(known - m2));
         }
-        *m_s = m2;
-        const float a = m == -INFINITY ? 0.0f : ex2(m - m2);
-        l *= a;
-        lx *= a;
         m = m2;
-        sum = sumx = 0.0f;
-        weights32(sa, f, m, w, 0, sum, bits, want_lse, sumx);
-        weights32(sa + 32, f, m, w, 16, sum, bits, want_lse, sumx);
       }
+      *m_s = m;
+      __threadfence_block();  // m before the turn
       __syncwarp();
-      if (lane == 0) mbar_arrive(settled(wl, quad, wh));
-      tc_st16(sa, w, 0);
-      tc_st16(sa + 16, w, 16);
-      l += sum;
-      lx += sumx;
+      if (lane == 0) turn[wh] = k + 1;
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full(wl, wh));
     }
-    if (ok && wh == 0 && !mbar_wait(settled(wl, quad, 1), (nk - 1) & 1)) ok = false;
+    if (ok && wh == 0 && !wait_turn(turn + 1, nk)) ok = false;
     if (ok) {  // half 1's last m is the row's
-      const float m2 = *m_s, a = m == -INFINITY ? 0.0f : ex2(m - m2);
+      const float m2 = *m_s, a = m == m2 ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - m2);
       l *= a;
       lx *= a;
       m = m2;
