@@ -49,8 +49,9 @@ using dc::smem_addr;
 constexpr int kTile = 128;          // tokens per tile
 constexpr int kBlock = 128;         // query rows per block
 constexpr int kThreads = 28 * 32;   // seven whole warpgroups, at 72 registers a thread
-constexpr int kDecodeWarp = 16, kMmaWarp = 24, kTmaWarp = 26;  // one MMA warp per lane
-constexpr int kKStages = 2;
+constexpr int kDecodeWarp = 16, kMmaWarp = 24, kTmaWarp = 25;
+constexpr int kKStages = 2, kVStages = 3;
+constexpr int kLogitBufs = 3;       // tiles whose logits or weights are in TMEM
 constexpr int kRing = 8;            // tiles whose key scales are kept (more than can be in flight)
 // A row's weights are 2^(logit - m) with m at least the largest logit so far and, when it is
 // set, kSlack above it: the check that a step stays below 2 is then one bit of the weights,
@@ -347,20 +348,19 @@ tree_prep_kernel(const TreeParams p, const TreeMma t, int row_ctas) {
 }
 
 // ---------------------------------------------------------------- main kernel
-template <int D, int R, bool V2, bool PAIR>
+template <int D, int R>
 struct Layout {
-  static constexpr int kVStages = PAIR ? 2 : 3;
   static constexpr int kOperand = operand_bytes(D, R);
   static constexpr int kVTile = kTile * D * 2;
   static constexpr int kQ = 0;
-  static constexpr int kK = kQ + (PAIR ? 2 : 1) * kOperand;
+  static constexpr int kK = kQ + kOperand;
   static constexpr int kV = kK + kKStages * kOperand;
-  static constexpr int kScale = kV + kVStages * kVTile;  // [kRing][kTile] floats
-  static constexpr int kMax = kScale + kRing * kTile * 4;  // [2 lanes][kBlock] floats: m of each row
-  static constexpr int kSums = kMax + 2 * kBlock * 4;      // [2 lanes][2 halves][kBlock] float2: sums of each row
-  static constexpr int kTurn = kSums + 4 * kBlock * 8;     // [2 lanes][4 quadrants][2 halves]: steps settled on an m
-  static constexpr int kBars = kTurn + 16 * 4;
-  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 12;
+  static constexpr int kScale = kV + kVStages * kVTile;   // [kRing][kTile] floats
+  static constexpr int kMax = kScale + kRing * kTile * 4; // [kBlock] floats: m of each row
+  static constexpr int kSums = kMax + kBlock * 4;         // [4 warpgroups][kBlock] float2: sums of each row
+  static constexpr int kTurn = kSums + 4 * kBlock * 8;    // [4 quadrants]: steps settled on an m
+  static constexpr int kBars = kTurn + 16;
+  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 3 * kLogitBufs + 2;
   static constexpr int kMisc = (kBars + 8 * kNumBars + 15) & ~15;  // tmem base, bad-value flag, 2 x 8 maxima
   static constexpr int kBytes = kMisc + 128 + 1024;    // and room for the alignment
 };
@@ -557,14 +557,13 @@ __device__ __forceinline__ float scale_weights(uint32_t ts, int n, float a) {
 
 // The sum of channel `ch` over the new tokens that row i sees and whose value there is not
 // finite once rounded to bf16 (they were left out of the value tiles).
-template <bool V2, bool PAIR>
+template <bool V2>
 __device__ __forceinline__ float bad_values(const TreeParams& p, const uint32_t* words, int wpr, int i, int b, int kv,
-                                         int lo, int t_lo, int t_hi, int P, int wl, int ch) {
+                                            int lo, int t_hi, int P, int ch) {
   float sum = 0.0f;
   const int d = p.c.d, ng = d / 32;
 #pragma unroll 1
   for (int tt = lo; tt < t_hi; ++tt) {
-    if (!PAIR && (((tt - t_lo) / kTile) & 1) != wl) continue;
     if (!((mask_word(words, wpr, i, (tt - P) >> 5) >> ((tt - P) & 31)) & 1u)) continue;
     const size_t row = cache_row_read(p.c, b, kv, tt, p.err);
     const float v = V2 ? fmaf(static_cast<float>(code2(p.c.v_codes + row * (d / 4), ch)),
@@ -575,32 +574,30 @@ __device__ __forceinline__ float bad_values(const TreeParams& p, const uint32_t*
   return sum;
 }
 
-template <int D, int R, bool V2, bool PAIR>
+template <int D, int R, bool V2>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUtensorMap vmap) {
-  using Ly = Layout<D, R, V2, PAIR>;
+  using Ly = Layout<D, R>;
   constexpr int NG = D / 32;
-  constexpr int VS = Ly::kVStages;
+  constexpr int VS = kVStages;
   extern __shared__ uint8_t raw_smem[];
 
   const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
   const int unit = blockIdx.z, b = unit / p.c.Hkv, kv = unit - b * p.c.Hkv;
   const SpanSeq sq = span_seq(p.span, b);
-  const int rows = sq.n * p.G, xb = blockIdx.x * (PAIR ? 2 : 1) * kBlock;
+  const int rows = sq.n * p.G, xb = blockIdx.x * kBlock;
   if (xb >= rows) return;
   const int P = sq.p0, L = sq.p0 < 0 ? 0 : sq.p0 + sq.n;
   const int t_lo = blockIdx.y * p.chunk, t_hi = min(L, t_lo + p.chunk);
   const int tiles = t_hi > t_lo ? (t_hi - t_lo + kTile - 1) / kTile : 0;
-  const int lane_parts = p.splits / gridDim.y;  // 2 when the lanes end as two splits
   const size_t part_rows = static_cast<size_t>(p.span.n) * p.G;
-  // this softmax thread's query row
-  const int wl = (warp >> 3) & 1, wh = (warp >> 2) & 1;  // lane and half of the softmax warp
-  const int x = xb + (PAIR ? wl * kBlock : 0) + (warp & 3) * 32 + lane;
+  // a softmax thread's query row; its warpgroup takes half wg & 1 of every other tile
+  const int wg = warp >> 2, quad = warp & 3, x = xb + quad * 32 + lane;
 
   if (tiles == 0) {  // nothing to read: the rows' share of this split is empty
-    if (warp < kDecodeWarp && wh == 0 && x < rows && (PAIR || wl < lane_parts)) {
+    if (warp < 4 && x < rows) {
       if (p.splits > 1) {
-        p.part_ml[(static_cast<size_t>(unit) * p.splits + blockIdx.y * lane_parts + (PAIR ? 0 : wl)) * part_rows + x] =
+        p.part_ml[(static_cast<size_t>(unit) * p.splits + blockIdx.y) * part_rows + x] =
             make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
       } else {
         const int i = x / p.G, h = kv * p.G + x - i * p.G;
@@ -623,34 +620,28 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   auto k_empty = [&](int s) { return bars + 8 * (1 + kKStages + s); };
   auto v_full = [&](int s) { return bars + 8 * (1 + 2 * kKStages + s); };
   auto v_empty = [&](int s) { return bars + 8 * (1 + 2 * kKStages + VS + s); };
-  // per lane l and half h (64 tokens) of its tile: logits written, weights written, readout done
-  auto s_full = [&](int l, int h) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + 2 * l + h); };
-  auto p_full = [&](int l, int h) { return bars + 8 * (5 + 2 * kKStages + 2 * VS + 2 * l + h); };
-  auto o_done = [&](int l, int h) { return bars + 8 * (9 + 2 * kKStages + 2 * VS + 2 * l + h); };
-  // tiles of lane l: PAIR all of them (when the lane has rows), else those of its parity
-  const int lanes_on = PAIR ? (xb + kBlock < rows ? 2 : 1) : (tiles > 1 ? 2 : 1);
-  auto lane_tiles = [&](int l) { return l >= lanes_on ? 0 : PAIR ? tiles : (tiles - l + 1) / 2; };
-  auto tile_of = [&](int l, int k) { return PAIR ? k : 2 * k + l; };
+  // per logit buffer: logits written, weights of half h (64 tokens) written; readout of half h
+  // of a tile done
+  auto s_full = [&](int s) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + s); };
+  auto p_full = [&](int s, int h) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + kLogitBufs + 2 * s + h); };
+  auto o_done = [&](int h) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + 3 * kLogitBufs + h); };
 
-  if (tid < 16) reinterpret_cast<int*>(sm + Ly::kTurn)[tid] = 0;
+  if (tid < 4) reinterpret_cast<int*>(sm + Ly::kTurn)[tid] = 0;
   if (tid == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(k_full(s), 8);
-      mbar_init(k_empty(s), PAIR ? lanes_on : 1);
+      mbar_init(k_empty(s), 1);
     }
     for (int s = 0; s < VS; ++s) {
       mbar_init(v_full(s), V2 ? 8 : 1);
-      mbar_init(v_empty(s), PAIR ? lanes_on : 1);
+      mbar_init(v_empty(s), 1);
     }
-    for (int l = 0; l < 2; ++l) {
-      const int r0 = rows - xb - (PAIR ? l * kBlock : 0);
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(s_full(l, h), 1);
-        mbar_init(p_full(l, h), max(1, min(4, (r0 + 31) / 32)));  // warps that have rows
-        mbar_init(o_done(l, h), 1);
-      }
+    for (int s = 0; s < kLogitBufs; ++s) {
+      mbar_init(s_full(s), 1);
+      for (int h = 0; h < 2; ++h) mbar_init(p_full(s, h), min(4, (rows - xb + 31) / 32));  // warps that have rows
     }
+    for (int h = 0; h < 2; ++h) mbar_init(o_done(h), 1);
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
@@ -662,15 +653,14 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc), tmem_o = tmem + kLogitBufs * kTile;
   bool ok = true;
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
-      const int nq = PAIR ? lanes_on : 1;
-      mbar_expect_tx(q_full, nq * Ly::kOperand);
+      mbar_expect_tx(q_full, Ly::kOperand);
       const uint8_t* img = t.qimg + (static_cast<size_t>(unit) * t.blocks + xb / kBlock) * Ly::kOperand;
-      dc::bulk_g2s(base + Ly::kQ, img, nq * Ly::kOperand, q_full);
+      dc::bulk_g2s(base + Ly::kQ, img, Ly::kOperand, q_full);
       if constexpr (!V2) {
         int issued = 0;
         for (int k = 0; k < tiles && ok; ++k) {
@@ -692,54 +682,55 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       }
       if (!mbar_wait(q_full, 0)) ok = false;
     }
-  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-    // One thread per lane.  Step -1: the logits of tile 0; step k: the readout of tile k, each
-    // half followed by its logits of tile k + 1, which overwrite the weights it read.
-    const int l = warp - kMmaWarp, n = lane_tiles(l);
-    if (lane == 0 && n > 0) {
-      constexpr uint32_t kLogit = mma_desc(0, 0, kTile / 2);  // fp16, both operands K-major
-      constexpr uint32_t kRead = mma_desc(1, 1, D);           // bf16, values channel-major
+  } else if (warp == kMmaWarp) {
+    // One thread.  Tile k's readout goes half by half as its weights come; between the two, the
+    // logits of tile k + 2, into the buffer of tile k - 1: two tiles ahead of the softmax.
+    if (lane == 0) {
+      constexpr uint32_t kLogit = mma_desc(0, 0, kTile);  // fp16, both operands K-major
+      constexpr uint32_t kRead = mma_desc(1, 1, D);       // bf16, values channel-major
       constexpr uint32_t kSwz = desc_hi(1024, 2), kFlat = desc_hi(128, 0);
       constexpr uint32_t kSide = D / 64 * (kTile * 128);  // the side entries within an operand
-      const uint32_t qa = base + Ly::kQ + (PAIR ? l * Ly::kOperand : 0);
-      const uint32_t q_lo = desc_lo(qa, 16), qs_lo = desc_lo(qa + kSide, kTile * 16);
+      const uint32_t q_lo = desc_lo(base + Ly::kQ, 16), qs_lo = desc_lo(base + Ly::kQ + kSide, kTile * 16);
       const uint32_t k_lo = desc_lo(base + Ly::kK, 16), ks_lo = desc_lo(base + Ly::kK + kSide, kTile * 16);
       const uint32_t v_lo = desc_lo(base + Ly::kV, kTile * 128);
       ok = mbar_wait(q_full, 0);
 #pragma unroll 1
-      for (int y = -2; y < 2 * n && ok; ++y) {
-        const int k = y >> 1, h = y & 1;
-        if (k >= 0) {
-          const int tile = tile_of(l, k), s = tile % VS;
-          if (h == 0 && !mbar_wait(v_full(s), (tile / VS) & 1)) { ok = false; break; }
-          if (!mbar_wait(p_full(l, h), k & 1)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t va = v_lo + ((s * Ly::kVTile + 8192 * h) >> 4), w = tmem + 128 * l + 64 * h;
+      for (int k = -2; k < tiles && ok; ++k) {
 #pragma unroll 1
-          for (int e = 0; e < 4; ++e)
-            tc_mma_ts(tmem + 256 + 128 * l, w + 8 * e, va + (2048 >> 4) * e, kSwz, kRead, y > 0 || e > 0);
-          tc_commit(o_done(l, h));
-          if (h == 1) tc_commit(v_empty(s));
-        }
-        if (k + 1 < n) {
-          const int tile = tile_of(l, k + 1), s = tile % kKStages;
-          if (h == 0 && !mbar_wait(k_full(s), (tile / kKStages) & 1)) { ok = false; break; }
-          if (k >= 0 && !mbar_wait(o_done(l, h), k & 1)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t ka = (s * Ly::kOperand + 8192 * h) >> 4, d = tmem + 128 * l + 64 * h;
-#pragma unroll 1
-          for (int e = 0; e < D / 16; ++e) {
-            const uint32_t off = ((e >> 2) * (kTile * 128) + 32 * (e & 3)) >> 4;
-            tc_mma_ss(d, q_lo + off, kSwz, k_lo + ka + off, kSwz, kLogit, e > 0);
+        for (int h = 0; h < 2 && ok; ++h) {
+          if (k >= 0) {
+            const int s = k % VS, buf = k % kLogitBufs;
+            if (h == 0 && !mbar_wait(v_full(s), (k / VS) & 1)) { ok = false; break; }
+            if (!mbar_wait(p_full(buf, h), (k / kLogitBufs) & 1)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t va = v_lo + ((s * Ly::kVTile + 8192 * h) >> 4), w = tmem + kTile * buf + 64 * h;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              tc_mma_ts(tmem_o, w + 8 * e, va + (2048 >> 4) * e, kSwz, kRead, k > 0 || h > 0 || e > 0);
+            tc_commit(o_done(h));
+            if (h == 1) tc_commit(v_empty(s));
           }
-          if constexpr (R > 0)
-            tc_mma_ss(d, qs_lo, kFlat, ks_lo + ((s * Ly::kOperand + 1024 * h) >> 4), kFlat, kLogit, true);
-          tc_commit(s_full(l, h));
-          if (h == 1) tc_commit(k_empty(s));
+          if (h == 0 && k + 2 < tiles) {
+            const int k2 = k + 2, s = k2 % kKStages, buf = k2 % kLogitBufs;
+            if (!mbar_wait(k_full(s), (k2 / kKStages) & 1) || (k > 0 && !mbar_wait(o_done(1), (k - 1) & 1))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t ka = (s * Ly::kOperand) >> 4, d = tmem + kTile * buf;
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) {
+              const uint32_t off = ((e >> 2) * (kTile * 128) + 32 * (e & 3)) >> 4;
+              tc_mma_ss(d, q_lo + off, kSwz, k_lo + ka + off, kSwz, kLogit, e > 0);
+            }
+            if constexpr (R > 0) tc_mma_ss(d, qs_lo, kFlat, ks_lo + ka, kFlat, kLogit, true);
+            tc_commit(s_full(buf));
+            tc_commit(k_empty(s));
+          }
         }
       }
       // the products are done before TMEM is given back
-      if (ok && !mbar_wait(o_done(l, 1), (n - 1) & 1)) ok = false;
+      if (ok && !mbar_wait(o_done(1), (tiles - 1) & 1)) ok = false;
     }
     __syncwarp();
   } else if (warp >= kDecodeWarp && warp < kMmaWarp) {
@@ -845,35 +836,32 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       }
       cur = nxt;
     }
-  } else if (warp < kDecodeWarp && xb + (PAIR ? wl * kBlock : 0) + (warp & 3) * 32 < rows && wl < lanes_on) {
+  } else if (warp < kDecodeWarp && xb + quad * 32 < rows) {
     // ---- softmax and epilogue of this warp's 32 query rows
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + 128 * wl + lane_off, to = tmem + 256 + 128 * wl + lane_off;
-    const int i = min(x, rows - 1) / p.G;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16, to = tmem_o + lane_off;
+    const int i = min(x, rows - 1) / p.G, wh = wg & 1;
     const float fq = t.qf[static_cast<size_t>(unit) * t.blocks * kBlock + x];
     const uint32_t* words = t.words ? t.words + (static_cast<size_t>(b) * p.span.n + i) * t.wpr : nullptr;
     const bool want_lse = p.lse != nullptr;
-    const int nk = lane_tiles(wl), quad = warp & 3;
     // tiles from here on hold new tokens or end the sequence
     const int tail_at = min(P, t_hi) >= t_lo ? (min(P, t_hi) - t_lo) / kTile : 0;
-    volatile float* m_s = reinterpret_cast<volatile float*>(sm + Ly::kMax) + wl * kBlock + quad * 32 + lane;
-    volatile int* turn = reinterpret_cast<volatile int*>(sm + Ly::kTurn) + 8 * wl + 2 * quad;
-    const uint32_t sa = ts + kHalf * wh;
-    // The two halves of a tile are two warps' work, on one m (they share the accumulator).
-    // Each forms its weights with the m it knows, then takes its turn (half 0 of a tile, half
-    // 1, half 0 of the next: the order of the readouts anyway) to learn of the other's m and
-    // to raise it.
+    volatile float* m_s = reinterpret_cast<volatile float*>(sm + Ly::kMax) + quad * 32 + lane;
+    volatile int* turn = reinterpret_cast<volatile int*>(sm + Ly::kTurn) + quad;
+    // The halves of the tiles are the work of four warps in turn, on one m (they share the
+    // accumulator).  Each forms its weights with the m it knows, then takes its turn (the
+    // order of the readouts anyway) to learn of the others' m and to raise it.
     float m = -INFINITY, l = 0.0f, lx = 0.0f;
 #pragma unroll 1
-    for (int k = 0; k < nk; ++k) {
-      const int tile = tile_of(wl, k);
-      const float* col = scale_s + (tile % kRing) * kTile;
-      if (!mbar_wait_idle(s_full(wl, wh), k & 1)) { ok = false; break; }
+    for (int k = wg >> 1; k < tiles; k += 2) {
+      const int buf = k % kLogitBufs;
+      const uint32_t sa = tmem + lane_off + kTile * buf + kHalf * wh;
+      const float* col = scale_s + (k % kRing) * kTile;
+      if (!mbar_wait_idle(s_full(buf), (k / kLogitBufs) & 1)) { ok = false; break; }
       tc_fence_after();
       float f = fmaxf(fq * col[0], 1e-37f);
-      if (tile >= tail_at) {
+      if (k >= tail_at) {
         f = fmaxf(fq, 1e-37f);
-        mask_half(sa, words, t.wpr, i, t_lo + tile * kTile + kHalf * wh - P, col + kHalf * wh);
+        mask_half(sa, words, t.wpr, i, t_lo + k * kTile + kHalf * wh - P, col + kHalf * wh);
       }
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {  // 32 tokens each, by one piece of code: the roles share the instruction cache
@@ -900,8 +888,8 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         }
         tc_st16(sa + 16 * c, w, 0);
       }
-      // this half's turn: the two halves agree on the larger m
-      if (!wait_turn(turn + 1 - wh, k + wh)) { ok = false; break; }
+      // this half's turn: all agree on the larger m
+      if (!wait_turn(turn, 2 * k + wh)) { ok = false; break; }
       const bool first = k == 0 && wh == 0;
       const float known = first ? m : *m_s;
       if (__any_sync(kAll, known != m)) {
@@ -915,7 +903,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         }
         if (!first && __any_sync(kAll, m2 > known)) {
           // the accumulator rests once the half before this one is read out
-          if (!mbar_wait(o_done(wl, 1 - wh), (wh ? k : k - 1) & 1)) ok = false;
+          if (!mbar_wait(o_done(1 - wh), (wh ? k : k - 1) & 1)) ok = false;
           tc_fence_after();
           scale_output<D>(to, known == -INFINITY ? 0.0f : ex2(known - m2));
         }
@@ -924,39 +912,42 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       *m_s = m;
       __threadfence_block();  // m before the turn
       __syncwarp();
-      if (lane == 0) turn[wh] = k + 1;
+      if (lane == 0) *turn = 2 * k + wh + 1;
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(wl, wh));
+      if (lane == 0) mbar_arrive(p_full(buf, wh));
     }
-    if (ok && wh == 0 && !wait_turn(turn + 1, nk)) ok = false;
-    if (ok) {  // half 1's last m is the row's
+    if (ok && !wait_turn(turn, 2 * tiles)) ok = false;
+    if (ok) {  // the last half's m is the row's
       const float m2 = *m_s, a = m == m2 ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - m2);
       l *= a;
       lx *= a;
       m = m2;
     }
-    float2* sums = reinterpret_cast<float2*>(sm + Ly::kSums) + 2 * wl * kBlock + quad * 32 + lane;
-    sums[wh * kBlock] = make_float2(l, lx);
-    asm volatile("bar.sync %0, 64;" ::"r"(2 + 4 * wl + quad) : "memory");
-    l += sums[(1 - wh) * kBlock].x;
-    lx += sums[(1 - wh) * kBlock].y;
-    if (ok && !mbar_wait(o_done(wl, 1), (nk - 1) & 1)) ok = false;
+    float2* sums = reinterpret_cast<float2*>(sm + Ly::kSums) + quad * 32 + lane;
+    sums[wg * kBlock] = make_float2(l, lx);
+    asm volatile("bar.sync %0, 128;" ::"r"(2 + quad) : "memory");
+    l = lx = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      l += sums[g * kBlock].x;
+      lx += sums[g * kBlock].y;
+    }
+    if (ok && !mbar_wait(o_done(1), (tiles - 1) & 1)) ok = false;
     tc_fence_after();
     if (ok) {
       const bool bad = *reinterpret_cast<volatile uint32_t*>(misc + 1) != 0u;
       const bool direct = p.splits == 1;
-      const int part = blockIdx.y * lane_parts + (PAIR ? 0 : wl);
-      const size_t pr = (static_cast<size_t>(unit) * p.splits + part) * part_rows + x;
+      const size_t pr = (static_cast<size_t>(unit) * p.splits + blockIdx.y) * part_rows + x;
       const int h = kv * p.G + x - i * p.G;
       const size_t orow = static_cast<size_t>(sq.row0) + i;
       const float inv = !direct ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+      constexpr int kCols = D / 4;  // each warpgroup's channels
       if (bad) {  // rare: one column at a time, in TMEM
 #pragma unroll 1
-        for (int c = wh * (D / 2); c < (wh + 1) * (D / 2); ++c) {
-          const float add = bad_values<V2, PAIR>(p, words, t.wpr, i, b, kv, max(P, t_lo), t_lo, t_hi, P, wl,
-                                                 V2 ? channel_at(c) : c);
+        for (int c = wg * kCols; c < (wg + 1) * kCols; ++c) {
+          const float add = bad_values<V2>(p, words, t.wpr, i, b, kv, max(P, t_lo), t_hi, P, V2 ? channel_at(c) : c);
           uint32_t w;
           asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(w) : "r"(to + c));
           tc_wait_ld();
@@ -966,35 +957,27 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         tc_wait_st();
       }
 #pragma unroll 1
-      for (int c = wh * (D / 64); c < (wh + 1) * (D / 64); ++c) {  // half the channels each
-        uint32_t w[32];
-        tc_ld32(to + 32 * c, w, 0);
+      for (int c = wg * kCols; c < (wg + 1) * kCols; c += 16) {
+        uint32_t w[16];
+        tc_ld16(to + c, w);
         tc_wait_ld();
-        float o[32];  // in channel order
+        float o[16];  // in channel order
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[V2 ? channel_at(j) : j] = __uint_as_float(w[j]);
-        if (l == 0.0f) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-        }
+        for (int j = 0; j < 16; ++j) o[V2 ? channel_at(j) : j] = l == 0.0f ? 0.0f : __uint_as_float(w[j]) * inv;
         if (x < rows) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 v = make_float4(o[j] * inv, o[j + 1] * inv, o[j + 2] * inv, o[j + 3] * inv);
-            if (direct) store_row4(p.out, orow * p.out.row_stride + h * p.out.head_stride + 32 * c + j, v);
-            else *reinterpret_cast<float4*>(p.part_o + pr * D + 32 * c + j) = v;
+          for (int j = 0; j < 16; j += 4) {
+            const float4 v = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            if (direct) store_row4(p.out, orow * p.out.row_stride + h * p.out.head_stride + c + j, v);
+            else *reinterpret_cast<float4*>(p.part_o + pr * D + c + j) = v;
           }
         }
       }
-      if (wh == 0 && x < rows) {
+      if (wg == 0 && x < rows) {
         if (!direct) p.part_ml[pr] = make_float4(m * dc::kLn2, l, lx, 0.0f);
         else if (want_lse) p.lse[orow * p.Hq + h] = l == 0.0f ? -INFINITY : m * dc::kLn2 + logf(lx);
       }
     }
-  } else if (warp < kDecodeWarp && wh == 0 && x < rows && !PAIR && wl < lane_parts) {
-    // the lane without a tile: its split is empty
-    p.part_ml[(static_cast<size_t>(unit) * p.splits + blockIdx.y * lane_parts + wl) * part_rows + x] =
-        make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
   }
 
   if (!ok) atomicOr(p.err, kDevErrWaitTimeout);
@@ -1006,8 +989,8 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <int D, int R, bool V2, bool PAIR>
-cudaError_t launch_main(const TreeParams& p, const TreeMma& t, int grid_splits, cudaStream_t s) {
+template <int D, int R, bool V2>
+cudaError_t launch_main(const TreeParams& p, const TreeMma& t, cudaStream_t s) {
   CUtensorMap map{};
   if (!V2) {
     const uint64_t slabs = p.c.page_size ? static_cast<uint64_t>(p.c.num_pages) * p.c.Hkv
@@ -1015,29 +998,25 @@ cudaError_t launch_main(const TreeParams& p, const TreeMma& t, int grid_splits, 
     const uint64_t rows = p.c.page_size ? p.c.page_size : p.c.T_cap;
     if (!encode_bf16_rows(&map, p.c.v, D, rows, slabs, 64)) return cudaErrorInvalidValue;
   }
-  auto k = tree_mma_kernel<D, R, V2, PAIR>;
-  constexpr int smem = Layout<D, R, V2, PAIR>::kBytes;
+  auto k = tree_mma_kernel<D, R, V2>;
+  constexpr int smem = Layout<D, R>::kBytes;
   static_assert(smem <= 232448, "shared memory of one CTA");
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  dim3 grid((t.blocks + (PAIR ? 1 : 0)) / (PAIR ? 2 : 1), grid_splits, p.c.B * p.c.Hkv);
+  dim3 grid(t.blocks, p.splits, p.c.B * p.c.Hkv);
   k<<<grid, kThreads, smem, s>>>(p, t, map);
   return cudaGetLastError();
 }
 
 template <int D, int R>
-cudaError_t launch_dr(const TreeParams& p, const TreeMma& t, int grid_splits, bool pair, cudaStream_t s) {
+cudaError_t launch_dr(const TreeParams& p, const TreeMma& t, cudaStream_t s) {
   const long long warps = static_cast<long long>(p.c.B) * p.c.Hkv * t.blocks * (kBlock / kPrepRows);
   const int row_ctas = static_cast<int>((warps + 7) / 8);
   const int mask_ctas = t.words ? (p.c.B * p.span.n + 7) / 8 : 0;
   tree_prep_kernel<D, R><<<row_ctas + mask_ctas, 256, 0, s>>>(p, t, row_ctas);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (p.c.vmode == HEADQ_V_2BIT)
-    return pair ? launch_main<D, R, true, true>(p, t, grid_splits, s)
-                : launch_main<D, R, true, false>(p, t, grid_splits, s);
-  return pair ? launch_main<D, R, false, true>(p, t, grid_splits, s)
-              : launch_main<D, R, false, false>(p, t, grid_splits, s);
+  return p.c.vmode == HEADQ_V_2BIT ? launch_main<D, R, true>(p, t, s) : launch_main<D, R, false>(p, t, s);
 }
 
 }  // namespace
@@ -1049,15 +1028,15 @@ bool tree_mma_supported(const headq_cache& c) {
 
 size_t tree_mma_image_bytes(const headq_cache& c) { return operand_bytes(c.d, c.r); }
 
-cudaError_t launch_tree_mma(const TreeParams& p, const TreeMma& t, int grid_splits, bool pair, cudaStream_t s) {
+cudaError_t launch_tree_mma(const TreeParams& p, const TreeMma& t, cudaStream_t s) {
   if (p.c.d == 128) {
-    if (p.c.r == 16) return launch_dr<128, 16>(p, t, grid_splits, pair, s);
-    if (p.c.r == 8) return launch_dr<128, 8>(p, t, grid_splits, pair, s);
-    return launch_dr<128, 0>(p, t, grid_splits, pair, s);
+    if (p.c.r == 16) return launch_dr<128, 16>(p, t, s);
+    if (p.c.r == 8) return launch_dr<128, 8>(p, t, s);
+    return launch_dr<128, 0>(p, t, s);
   }
-  if (p.c.r == 16) return launch_dr<64, 16>(p, t, grid_splits, pair, s);
-  if (p.c.r == 8) return launch_dr<64, 8>(p, t, grid_splits, pair, s);
-  return launch_dr<64, 0>(p, t, grid_splits, pair, s);
+  if (p.c.r == 16) return launch_dr<64, 16>(p, t, s);
+  if (p.c.r == 8) return launch_dr<64, 8>(p, t, s);
+  return launch_dr<64, 0>(p, t, s);
 }
 
 }  // namespace headq
