@@ -35,7 +35,7 @@ struct TreeWs {
 TreeWs tree_ws(const headq_cache& c, int Hq, int n, const TreePlan& tp) {
   TreeWs w{};
   const size_t units = static_cast<size_t>(c.B) * c.Hkv;
-  const size_t rows = tp.splits > 1 ? static_cast<size_t>(c.B) * Hq * n * tp.splits : 0;
+  const size_t rows = tp.parts > 1 ? static_cast<size_t>(c.B) * Hq * n * tp.parts : 0;
   w.part_ml = kWsHeaderBytes + round256(rows * c.d * sizeof(float));
   w.qimg = w.part_ml + round256(rows * sizeof(float4));
   w.qf = w.qimg + (tp.mma ? round256(units * tp.blocks * tree_mma_image_bytes(c)) : 0);
@@ -152,7 +152,7 @@ HEADQ_API headq_status headq_tree_attn(const headq_cache* cache, const headq_row
   p.sm_scale = sm_scale;
   p.corr_sign = static_cast<float>(corr_sign);
   p.lse = lse;
-  p.splits = tp.splits;
+  p.splits = tp.parts;
   p.chunk = tp.chunk;
   uint8_t* base = static_cast<uint8_t*>(ws);
   p.err = reinterpret_cast<unsigned*>(base);

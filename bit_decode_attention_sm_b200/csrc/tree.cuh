@@ -5,11 +5,12 @@
 
 namespace headq {
 
-// How a call runs: on the tensor cores (tree_mma.cu, `blocks` blocks of 128 query rows per
-// sequence and KV head) or in fp32 (tree_attn.cu), in `splits` T-splits of `chunk` tokens.
+// How a call runs: on the tensor cores (tree_mma.cu) with one or (pair) two 128-row blocks
+// per CTA, or in fp32 (tree_attn.cu); grid_splits T-splits of `chunk` tokens per (sequence,
+// KV head), which leave `parts` partial results to merge (1: none).
 struct TreePlan {
-  bool mma;
-  int blocks, splits, chunk;
+  bool mma, pair;
+  int blocks, grid_splits, parts, chunk;
 };
 TreePlan tree_plan(const headq_cache& c, int Hq, int n, int T, bool q_bf16);
 
@@ -24,7 +25,7 @@ struct TreeMma {
 };
 bool tree_mma_supported(const headq_cache& c);
 size_t tree_mma_image_bytes(const headq_cache& c);
-cudaError_t launch_tree_mma(const TreeParams& p, const TreeMma& t, cudaStream_t s);
+cudaError_t launch_tree_mma(const TreeParams& p, const TreeMma& t, int grid_splits, bool pair, cudaStream_t s);
 cudaError_t launch_tree(const TreeParams& p, const TreeMma& t, const TreePlan& plan, cudaStream_t s);
 
 // whether new token i of sequence b sees its new token j (both below span.n)

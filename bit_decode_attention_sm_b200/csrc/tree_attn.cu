@@ -287,28 +287,31 @@ cudaError_t launch_merge(const TreeParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// Tensor cores: one CTA per SM, so the splits that minimise waves x (tiles per CTA + 4),
-// the 4 standing for a CTA's set-up, first loads and epilogue.  fp32 kernel: about four
+// Tensor cores: one CTA per SM, so the splits that minimise waves x (tiles per CTA + 3),
+// the 3 standing for a CTA's set-up, first loads and epilogue.  fp32 kernel: about four
 // CTAs per SM, chunks of whole 32-token tiles.
 TreePlan tree_plan(const headq_cache& c, int Hq, int n, int T, bool q_bf16) {
   const long long units = static_cast<long long>(c.B) * c.Hkv, rows = static_cast<long long>(n) * (Hq / c.Hkv);
-  TreePlan tp{q_bf16 && tree_mma_supported(c), static_cast<int>((rows + 127) / 128), 1, 128};
+  TreePlan tp{q_bf16 && tree_mma_supported(c), false, static_cast<int>((rows + 127) / 128), 1, 1, 128};
   if (n <= 0 || units <= 0) return tp;
   const int sms = sm_count();
   if (tp.mma) {
-    const long long ctas = units * tp.blocks;
+    tp.pair = tp.blocks > 1;
+    const long long ctas = units * (tp.pair ? (tp.blocks + 1) / 2 : tp.blocks);
     const int tiles = T > 128 ? (T + 127) / 128 : 1;
     long long best = -1;
     for (int s = 1; s <= tiles && s <= sms; ++s) {
       const int per = (tiles + s - 1) / s, used = (tiles + per - 1) / per;
       if (used != s) continue;
-      const long long cost = ((ctas * s + sms - 1) / sms) * (per + 4) + (s > 1 ? 2 : 0);
+      const long long cost = ((ctas * s + sms - 1) / sms) * (per + 3) + (s > 1 ? 1 : 0);
       if (best < 0 || cost < best) {
         best = cost;
-        tp.splits = s;
+        tp.grid_splits = s;
         tp.chunk = per * 128;
       }
     }
+    // the two lanes of a CTA that take alternate tiles end as two parts
+    tp.parts = tp.grid_splits * (!tp.pair && tp.chunk > 128 ? 2 : 1);
     return tp;
   }
   const int tiles = T > kTT ? (T + kTT - 1) / kTT : 1;
@@ -317,15 +320,15 @@ TreePlan tree_plan(const headq_cache& c, int Hq, int n, int T, bool q_bf16) {
   if (s > tiles) s = tiles;
   const int per = static_cast<int>((tiles + s - 1) / s);
   tp.chunk = per * kTT;
-  tp.splits = (tiles + per - 1) / per;
+  tp.grid_splits = tp.parts = (tiles + per - 1) / per;
   return tp;
 }
 
 cudaError_t launch_tree(const TreeParams& p, const TreeMma& t, const TreePlan& plan, cudaStream_t s) {
   cudaError_t e = cudaErrorInvalidValue;
   if (plan.mma) {
-    e = launch_tree_mma(p, t, s);
-    if (e != cudaSuccess || plan.splits == 1) return e;
+    e = launch_tree_mma(p, t, plan.grid_splits, plan.pair, s);
+    if (e != cudaSuccess || plan.parts == 1) return e;
     return p.c.d == 128 ? launch_merge<128>(p, s) : launch_merge<64>(p, s);
   }
 #define HEADQ_TREE_D(D)                                              \

@@ -11,7 +11,7 @@
 //   power of two (exact for bf16 queries but for elements 2^-28 below the row's largest),
 //   U_h^T q behind them, written as the shared-memory image the main kernel copies in; the
 //   mask as bits.
-// tree_mma_kernel    one CTA of 28 warps per (row blocks, split, sequence x KV head):
+// tree_mma_kernel    one CTA of 20 warps per (row blocks, split, sequence x KV head):
 //   8 decoder warps  two threads per token, half the channels each: packed codes from HBM (the next tile's loads in
 //     flight) to fp16 keys in shared memory, scaled by a power of two per tile.  The four
 //     levels min + code * scale of a 32-channel group are rounded to fp16 once, two 2-bit
@@ -19,8 +19,8 @@
 //     transpose within each 16, and the queries are stored in that order too.  2-bit values
 //     the same way in bf16.
 //   1 TMA warp       dense bf16 values, 64 tokens x 64 channels a box
-//   2 MMA threads    one per lane (below): logits into TMEM, readout from the weights there
-//   2 x 2 x 4 softmax warps: two "lanes", in each one thread per query row and half a tile.  PAIR (more than 128 rows):
+//   2 MMA warps      one per lane (below): logits into TMEM, readout from the weights there
+//   2 x 4 softmax warps (two "lanes"), one thread per query row.  PAIR (more than 128 rows):
 //     the lanes hold two row blocks over the same tiles, so each decoded tile serves 256
 //     rows; else they take alternate tiles of the one block and end as two splits.
 // The running maximum is kept with a slack of 2^60 (kSlack): one pass over the logits and no
@@ -48,10 +48,12 @@ using dc::smem_addr;
 
 constexpr int kTile = 128;          // tokens per tile
 constexpr int kBlock = 128;         // query rows per block
-constexpr int kThreads = 28 * 32;   // seven whole warpgroups, at 72 registers a thread
-constexpr int kDecodeWarp = 16, kMmaWarp = 24, kTmaWarp = 25;
-constexpr int kKStages = 2, kVStages = 3;
-constexpr int kLogitBufs = 3;       // tiles whose logits or weights are in TMEM
+constexpr int kThreads = 20 * 32;  // five whole warpgroups
+// registers per thread after the split: 8 x 32 x 128 + 8 x 32 x 80 + 4 x 32 x 48 = 59392, of
+// the 640 x 96 = 61440 that the block holds at launch
+constexpr int kRegsSoftmax = 128, kRegsDecode = 80, kRegsOther = 48;
+constexpr int kDecodeWarp = 8, kMmaWarp = 16, kTmaWarp = 18;  // one MMA warp per lane
+constexpr int kKStages = 2;
 constexpr int kRing = 8;            // tiles whose key scales are kept (more than can be in flight)
 // A row's weights are 2^(logit - m) with m at least the largest logit so far and, when it is
 // set, kSlack above it: the check that a step stays below 2 is then one bit of the weights,
@@ -67,25 +69,33 @@ __host__ __device__ constexpr int operand_bytes(int d, int r) { return kTile * (
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-// descriptors as their two words: the high ones are constants, the low ones one addition apart
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
-                                          uint32_t idesc, bool acc) {
+// The next three are executed by the whole warp and take effect for the thread with `one`
+// set: their operands are then the same in every lane, and need no moves out of per-thread
+// registers between one product and the next.
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.u32 p, %6, 0;\n"
-      " mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, bool acc) {
+// descriptors as their two words
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
+                                          uint32_t idesc, bool acc, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.u32 p, %5, 0;\n"
+      "{\n .reg .pred p, q;\n .reg .b64 da, db;\n setp.ne.u32 p, %6, 0;\n setp.ne.u32 q, %7, 0;\n"
+      " mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, bool acc,
+                                          uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 db;\n setp.ne.u32 p, %5, 0;\n setp.ne.u32 q, %6, 0;\n"
       " mov.b64 db, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(one)
       : "memory");
 }
 template <int N>
@@ -156,19 +166,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   } while (clock64() - start < dc::kWaitCycles);
   return false;
 }
-// The same for the warps that wait long and are many: a short sleep between the tries leaves
-// the issue slots to the others.
-__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity) {
-  if (mbar_try(bar, parity)) return true;
-  const long long start = clock64();
-  do {
-#pragma unroll 1
-    for (int k = 0; k < 64; ++k) {
-      __nanosleep(32);
-      if (mbar_try(bar, parity)) return true;
-    }
-  } while (clock64() - start < dc::kWaitCycles);
-  return false;
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -348,19 +354,17 @@ tree_prep_kernel(const TreeParams p, const TreeMma t, int row_ctas) {
 }
 
 // ---------------------------------------------------------------- main kernel
-template <int D, int R>
+template <int D, int R, bool V2, bool PAIR>
 struct Layout {
+  static constexpr int kVStages = PAIR ? 2 : 3;
   static constexpr int kOperand = operand_bytes(D, R);
   static constexpr int kVTile = kTile * D * 2;
   static constexpr int kQ = 0;
-  static constexpr int kK = kQ + kOperand;
+  static constexpr int kK = kQ + (PAIR ? 2 : 1) * kOperand;
   static constexpr int kV = kK + kKStages * kOperand;
-  static constexpr int kScale = kV + kVStages * kVTile;   // [kRing][kTile] floats
-  static constexpr int kMax = kScale + kRing * kTile * 4; // [kBlock] floats: m of each row
-  static constexpr int kSums = kMax + kBlock * 4;         // [4 warpgroups][kBlock] float2: sums of each row
-  static constexpr int kTurn = kSums + 4 * kBlock * 8;    // [4 quadrants]: steps settled on an m
-  static constexpr int kBars = kTurn + 16;
-  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 3 * kLogitBufs + 2;
+  static constexpr int kScale = kV + kVStages * kVTile;  // [kRing][kTile] floats
+  static constexpr int kBars = kScale + kRing * kTile * 4;
+  static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 12;
   static constexpr int kMisc = (kBars + 8 * kNumBars + 15) & ~15;  // tmem base, bad-value flag, 2 x 8 maxima
   static constexpr int kBytes = kMisc + 128 + 1024;    // and room for the alignment
 };
@@ -457,61 +461,32 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int wpr, int 
   return __funnelshift_r(mask_word(row, wpr, i, k), mask_word(row, wpr, i, k + 1), a & 31);
 }
 
-// kSlack above the largest of 32 logits (times f), or -inf
-__device__ __forceinline__ float row_max(const uint32_t (&u)[32], float f) {
-  float mx = __uint_as_float(u[0]);
-#pragma unroll
-  for (int j = 1; j < 31; j += 2) mx = max3(mx, __uint_as_float(u[j]), __uint_as_float(u[j + 1]));
-  return fmaxf(mx, __uint_as_float(u[31])) * f + kSlack;
-}
+// Running maximum (log2 units), sum of the truncated weights, sum of the exact ones.
+struct RowState {
+  float m, l, lx;
+};
 
-// 32 logits of this thread's row (times f: log2 units) to weights relative to 2^m, two to a
-// word; their sum, and all their bits
-__device__ __forceinline__ void weights32(const uint32_t (&u)[32], float f, float m, uint32_t (&w)[16], float& sum,
-                                          uint32_t& bits) {
-  const float mm = m == -INFINITY ? 0.0f : m;
-  const uint64_t f2 = codec::pk2(f, f), m2 = codec::pk2(-mm, -mm);
-  uint64_t a[2] = {0ull, 0ull};
-  bits = 0u;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint64_t y = codec::fma2(codec::pk2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])), f2, m2);
-    const uint32_t h0 = __float_as_uint(ex2(codec::pk_lo(y))) & 0xffff0000u;
-    const uint32_t h1 = __float_as_uint(ex2(codec::pk_hi(y))) & 0xffff0000u;
-    w[j] = __byte_perm(h0, h1, 0x7632);
-    bits |= w[j];
-    a[j & 1] = codec::add2(a[j & 1], codec::pk2(__uint_as_float(h0), __uint_as_float(h1)));
-  }
-  const uint64_t t = codec::add2(a[0], a[1]);
-  sum = codec::pk_lo(t) + codec::pk_hi(t);
-}
-
-// Wait until the other half's warp has settled `steps` steps (a word in shared memory: a
-// load, where a barrier would cost several times that); false after about 2 s.
-__device__ __forceinline__ bool wait_turn(const volatile int* turn, int steps) {
-  if (*turn >= steps) return true;
-  const long long start = clock64();
-#pragma unroll 1
-  while (*turn < steps) {
-    __nanosleep(32);
-    if (clock64() - start > dc::kWaitCycles) return false;
-  }
-  return true;
-}
-
-// The accumulator of this thread's row times a.
+// The rows whose m rises (to `top`; the others pass their m): their sums and their
+// accumulator scaled to it.
 template <int D>
-__device__ __forceinline__ void scale_output(uint32_t to, float a) {
+__device__ __forceinline__ RowState raise_max(RowState st, float top, uint32_t to, bool have_o) {
+  const float a = st.m == -INFINITY ? 0.0f : ex2(st.m - top);
+  st.l *= a;
+  st.lx *= a;
+  st.m = top;
+  if (have_o) {
 #pragma unroll 1
-  for (int o = 0; o < D; o += 4) {
-    uint32_t w[4];
-    tc_ld4(to + o, w);
-    tc_wait_ld();
+    for (int o = 0; o < D; o += 4) {  // few registers: half a row of logits is held meanwhile
+      uint32_t w[4];
+      tc_ld4(to + o, w);
+      tc_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * a);
-    tc_st4(to + o, w);
+      for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * a);
+      tc_st4(to + o, w);
+    }
+    tc_wait_st();
   }
-  tc_wait_st();
+  return st;
 }
 
 constexpr int kHalf = kTile / 2;
@@ -533,37 +508,39 @@ __device__ __forceinline__ void mask_half(uint32_t ts, const uint32_t* row, int 
   tc_wait_st();
 }
 
-// Weights two to a word, in TMEM columns [ts, ts + n): times a, truncated again; the change
-// that truncation makes to their sum.
-__device__ __forceinline__ float scale_weights(uint32_t ts, int n, float a) {
-  float change = 0.0f;
-#pragma unroll 1
-  for (int c = 0; c < n; c += 4) {
-    uint32_t w[4];
-    tc_ld4(ts + c, w);
-    tc_wait_ld();
+// Half a tile's 64 logits of this thread's row (times f: log2 units) to weights, two to a
+// word; their sum, and all their bits.  The 64 are in registers before the first
+// exponential, so that these run back to back.
+__device__ __forceinline__ void weights(const uint32_t (&s)[kHalf], float f, float m, uint32_t (&w)[kHalf / 2],
+                                        float& sum, uint32_t& bits) {
+  const float mm = m == -INFINITY ? 0.0f : m;
+  const uint64_t f2 = codec::pk2(f, f), m2 = codec::pk2(-mm, -mm);
+  uint64_t a[2] = {0ull, 0ull};
+  uint32_t any[2] = {0u, 0u};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float e0 = __uint_as_float(w[j] << 16) * a, e1 = __uint_as_float(w[j] & 0xffff0000u) * a;
-      const uint32_t h0 = __float_as_uint(e0) & 0xffff0000u, h1 = __float_as_uint(e1) & 0xffff0000u;
-      change += (__uint_as_float(h0) - e0) + (__uint_as_float(h1) - e1);
-      w[j] = (h0 >> 16) | h1;
-    }
-    tc_st4(ts + c, w);
+  for (int j = 0; j < kHalf / 2; ++j) {
+    const uint64_t y = codec::fma2(codec::pk2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), f2, m2);
+    const uint32_t h0 = __float_as_uint(ex2(codec::pk_lo(y))) & 0xffff0000u;
+    const uint32_t h1 = __float_as_uint(ex2(codec::pk_hi(y))) & 0xffff0000u;
+    w[j] = __byte_perm(h0, h1, 0x7632);
+    any[j & 1] |= w[j];
+    a[j & 1] = codec::add2(a[j & 1], codec::pk2(__uint_as_float(h0), __uint_as_float(h1)));
   }
-  tc_wait_st();
-  return change;
+  const uint64_t t = codec::add2(a[0], a[1]);
+  sum = codec::pk_lo(t) + codec::pk_hi(t);
+  bits = any[0] | any[1];
 }
 
 // The sum of channel `ch` over the new tokens that row i sees and whose value there is not
 // finite once rounded to bf16 (they were left out of the value tiles).
-template <bool V2>
+template <bool V2, bool PAIR>
 __device__ __forceinline__ float bad_values(const TreeParams& p, const uint32_t* words, int wpr, int i, int b, int kv,
-                                            int lo, int t_hi, int P, int ch) {
+                                         int lo, int t_lo, int t_hi, int P, int wl, int ch) {
   float sum = 0.0f;
   const int d = p.c.d, ng = d / 32;
 #pragma unroll 1
   for (int tt = lo; tt < t_hi; ++tt) {
+    if (!PAIR && (((tt - t_lo) / kTile) & 1) != wl) continue;
     if (!((mask_word(words, wpr, i, (tt - P) >> 5) >> ((tt - P) & 31)) & 1u)) continue;
     const size_t row = cache_row_read(p.c, b, kv, tt, p.err);
     const float v = V2 ? fmaf(static_cast<float>(code2(p.c.v_codes + row * (d / 4), ch)),
@@ -574,30 +551,32 @@ __device__ __forceinline__ float bad_values(const TreeParams& p, const uint32_t*
   return sum;
 }
 
-template <int D, int R, bool V2>
+template <int D, int R, bool V2, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUtensorMap vmap) {
-  using Ly = Layout<D, R>;
+  using Ly = Layout<D, R, V2, PAIR>;
   constexpr int NG = D / 32;
-  constexpr int VS = kVStages;
+  constexpr int VS = Ly::kVStages;
   extern __shared__ uint8_t raw_smem[];
 
   const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
   const int unit = blockIdx.z, b = unit / p.c.Hkv, kv = unit - b * p.c.Hkv;
   const SpanSeq sq = span_seq(p.span, b);
-  const int rows = sq.n * p.G, xb = blockIdx.x * kBlock;
+  const int rows = sq.n * p.G, xb = blockIdx.x * (PAIR ? 2 : 1) * kBlock;
   if (xb >= rows) return;
   const int P = sq.p0, L = sq.p0 < 0 ? 0 : sq.p0 + sq.n;
   const int t_lo = blockIdx.y * p.chunk, t_hi = min(L, t_lo + p.chunk);
   const int tiles = t_hi > t_lo ? (t_hi - t_lo + kTile - 1) / kTile : 0;
+  const int lane_parts = p.splits / gridDim.y;  // 2 when the lanes end as two splits
   const size_t part_rows = static_cast<size_t>(p.span.n) * p.G;
-  // a softmax thread's query row; its warpgroup takes half wg & 1 of every other tile
-  const int wg = warp >> 2, quad = warp & 3, x = xb + quad * 32 + lane;
+  // this softmax thread's query row
+  const int wl = (warp >> 2) & 1;  // lane of the softmax warp
+  const int x = xb + (PAIR ? wl * kBlock : 0) + (warp & 3) * 32 + lane;
 
   if (tiles == 0) {  // nothing to read: the rows' share of this split is empty
-    if (warp < 4 && x < rows) {
+    if (warp < 8 && x < rows && (PAIR || wl < lane_parts)) {
       if (p.splits > 1) {
-        p.part_ml[(static_cast<size_t>(unit) * p.splits + blockIdx.y) * part_rows + x] =
+        p.part_ml[(static_cast<size_t>(unit) * p.splits + blockIdx.y * lane_parts + (PAIR ? 0 : wl)) * part_rows + x] =
             make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
       } else {
         const int i = x / p.G, h = kv * p.G + x - i * p.G;
@@ -620,28 +599,34 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   auto k_empty = [&](int s) { return bars + 8 * (1 + kKStages + s); };
   auto v_full = [&](int s) { return bars + 8 * (1 + 2 * kKStages + s); };
   auto v_empty = [&](int s) { return bars + 8 * (1 + 2 * kKStages + VS + s); };
-  // per logit buffer: logits written, weights of half h (64 tokens) written; readout of half h
-  // of a tile done
-  auto s_full = [&](int s) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + s); };
-  auto p_full = [&](int s, int h) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + kLogitBufs + 2 * s + h); };
-  auto o_done = [&](int h) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + 3 * kLogitBufs + h); };
+  // per lane l and half h (64 tokens) of its tile: logits written, weights written, readout done
+  auto s_full = [&](int l, int h) { return bars + 8 * (1 + 2 * kKStages + 2 * VS + 2 * l + h); };
+  auto p_full = [&](int l, int h) { return bars + 8 * (5 + 2 * kKStages + 2 * VS + 2 * l + h); };
+  auto o_done = [&](int l, int h) { return bars + 8 * (9 + 2 * kKStages + 2 * VS + 2 * l + h); };
 
-  if (tid < 4) reinterpret_cast<int*>(sm + Ly::kTurn)[tid] = 0;
+  // tiles of lane l: PAIR all of them (when the lane has rows), else those of its parity
+  const int lanes_on = PAIR ? (xb + kBlock < rows ? 2 : 1) : (tiles > 1 ? 2 : 1);
+  auto lane_tiles = [&](int l) { return l >= lanes_on ? 0 : PAIR ? tiles : (tiles - l + 1) / 2; };
+  auto tile_of = [&](int l, int k) { return PAIR ? k : 2 * k + l; };
+
   if (tid == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(k_full(s), 8);
-      mbar_init(k_empty(s), 1);
+      mbar_init(k_empty(s), PAIR ? lanes_on : 1);
     }
     for (int s = 0; s < VS; ++s) {
       mbar_init(v_full(s), V2 ? 8 : 1);
-      mbar_init(v_empty(s), 1);
+      mbar_init(v_empty(s), PAIR ? lanes_on : 1);
     }
-    for (int s = 0; s < kLogitBufs; ++s) {
-      mbar_init(s_full(s), 1);
-      for (int h = 0; h < 2; ++h) mbar_init(p_full(s, h), min(4, (rows - xb + 31) / 32));  // warps that have rows
+    for (int l = 0; l < 2; ++l) {
+      const int r0 = rows - xb - (PAIR ? l * kBlock : 0);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(s_full(l, h), 1);
+        mbar_init(p_full(l, h), max(1, min(4, (r0 + 31) / 32)));  // warps that have rows
+        mbar_init(o_done(l, h), 1);
+      }
     }
-    for (int h = 0; h < 2; ++h) mbar_init(o_done(h), 1);
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
@@ -653,19 +638,23 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc), tmem_o = tmem + kLogitBufs * kTile;
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
   bool ok = true;
 
+  // Registers move from the other warps to the softmax warps, a warpgroup at a time.
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kTmaWarp) {
     if (lane == 0) {
-      mbar_expect_tx(q_full, Ly::kOperand);
+      const int nq = PAIR ? lanes_on : 1;
+      mbar_expect_tx(q_full, nq * Ly::kOperand);
       const uint8_t* img = t.qimg + (static_cast<size_t>(unit) * t.blocks + xb / kBlock) * Ly::kOperand;
-      dc::bulk_g2s(base + Ly::kQ, img, Ly::kOperand, q_full);
+      dc::bulk_g2s(base + Ly::kQ, img, nq * Ly::kOperand, q_full);
       if constexpr (!V2) {
         int issued = 0;
         for (int k = 0; k < tiles && ok; ++k) {
           const int s = k % VS;
-          if (k >= VS && !mbar_wait_idle(v_empty(s), ((k / VS) - 1) & 1)) { ok = false; break; }
+          if (k >= VS && !mbar_wait(v_empty(s), ((k / VS) - 1) & 1)) { ok = false; break; }
           const int t0 = t_lo + k * kTile;
           const int halves = t0 + 64 < t_hi ? 2 : 1;
           mbar_expect_tx(v_full(s), halves * 64 * D * 2);
@@ -682,58 +671,62 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       }
       if (!mbar_wait(q_full, 0)) ok = false;
     }
-  } else if (warp == kMmaWarp) {
-    // One thread.  Tile k's readout goes half by half as its weights come; between the two, the
-    // logits of tile k + 2, into the buffer of tile k - 1: two tiles ahead of the softmax.
-    if (lane == 0) {
-      constexpr uint32_t kLogit = mma_desc(0, 0, kTile);  // fp16, both operands K-major
-      constexpr uint32_t kRead = mma_desc(1, 1, D);       // bf16, values channel-major
-      constexpr uint32_t kSwz = desc_hi(1024, 2), kFlat = desc_hi(128, 0);
-      constexpr uint32_t kSide = D / 64 * (kTile * 128);  // the side entries within an operand
-      const uint32_t q_lo = desc_lo(base + Ly::kQ, 16), qs_lo = desc_lo(base + Ly::kQ + kSide, kTile * 16);
-      const uint32_t k_lo = desc_lo(base + Ly::kK, 16), ks_lo = desc_lo(base + Ly::kK + kSide, kTile * 16);
-      const uint32_t v_lo = desc_lo(base + Ly::kV, kTile * 128);
-      ok = mbar_wait(q_full, 0);
+  } else if (warp < kTmaWarp) {
+    // The halves of a lane's tile take turns: while the exponentials of one run, the other's
+    // readout and next logits do.
+    const int l = warp - kMmaWarp, n = lane_tiles(l);
+    constexpr uint32_t kLogit = mma_desc(0, 0, kTile / 2);  // fp16, both operands K-major
+    constexpr uint32_t kRead = mma_desc(1, 1, D);           // bf16, values channel-major
+    constexpr uint32_t kSwz = desc_hi(1024, 2), kFlat = desc_hi(128, 0);
+    constexpr uint32_t kSide = D / 64 * (kTile * 128);  // the side entries within an operand
+    const uint32_t one = lane == 0;
+    const uint32_t qa = base + Ly::kQ + (PAIR ? l * Ly::kOperand : 0);
+    const uint32_t q_lo = desc_lo(qa, 16), qs_lo = desc_lo(qa + kSide, kTile * 16);
+    const uint32_t k_lo = desc_lo(base + Ly::kK, 16), ks_lo = desc_lo(base + Ly::kK + kSide, kTile * 16);
+    const uint32_t v_lo = desc_lo(base + Ly::kV, kTile * 128);
+    auto wait = [&](uint32_t bar, int phase) {
+      ok = __all_sync(kAll, ok && mbar_wait(bar, phase & 1));
+      return ok;
+    };
+    // step -1: logits of tile 0; step k: readout of tile k, each half followed by its logits
+    // of tile k + 1, which overwrite the weights it read
+    if (n > 0) wait(q_full, 0);
 #pragma unroll 1
-      for (int k = -2; k < tiles && ok; ++k) {
-#pragma unroll 1
-        for (int h = 0; h < 2 && ok; ++h) {
-          if (k >= 0) {
-            const int s = k % VS, buf = k % kLogitBufs;
-            if (h == 0 && !mbar_wait(v_full(s), (k / VS) & 1)) { ok = false; break; }
-            if (!mbar_wait(p_full(buf, h), (k / kLogitBufs) & 1)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t va = v_lo + ((s * Ly::kVTile + 8192 * h) >> 4), w = tmem + kTile * buf + 64 * h;
+    for (int y = -2; y < 2 * n && ok; ++y) {
+      const int k = y >> 1, h = y & 1;
+      if (k >= 0) {
+        const int tile = tile_of(l, k), s = tile % VS;
+        if (!wait(p_full(l, h), k) || !wait(v_full(s), tile / VS)) break;
+        tc_fence_after();
+        const uint32_t va = v_lo + ((s * Ly::kVTile + 8192 * h) >> 4), w = tmem + 128 * l + 64 * h;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              tc_mma_ts(tmem_o, w + 8 * e, va + (2048 >> 4) * e, kSwz, kRead, k > 0 || h > 0 || e > 0);
-            tc_commit(o_done(h));
-            if (h == 1) tc_commit(v_empty(s));
-          }
-          if (h == 0 && k + 2 < tiles) {
-            const int k2 = k + 2, s = k2 % kKStages, buf = k2 % kLogitBufs;
-            if (!mbar_wait(k_full(s), (k2 / kKStages) & 1) || (k > 0 && !mbar_wait(o_done(1), (k - 1) & 1))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t ka = (s * Ly::kOperand) >> 4, d = tmem + kTile * buf;
-#pragma unroll
-            for (int e = 0; e < D / 16; ++e) {
-              const uint32_t off = ((e >> 2) * (kTile * 128) + 32 * (e & 3)) >> 4;
-              tc_mma_ss(d, q_lo + off, kSwz, k_lo + ka + off, kSwz, kLogit, e > 0);
-            }
-            if constexpr (R > 0) tc_mma_ss(d, qs_lo, kFlat, ks_lo + ka, kFlat, kLogit, true);
-            tc_commit(s_full(buf));
-            tc_commit(k_empty(s));
-          }
-        }
+        for (int e = 0; e < 4; ++e)
+          tc_mma_ts(tmem + 256 + 128 * l, w + 8 * e, va + (2048 >> 4) * e, kSwz, kRead, y > 0 || e > 0, one);
+        tc_commit(o_done(l, h), one);
+        if (h == 1) tc_commit(v_empty(s), one);
       }
-      // the products are done before TMEM is given back
-      if (ok && !mbar_wait(o_done(1), (tiles - 1) & 1)) ok = false;
+      if (k + 1 < n) {
+        const int tile = tile_of(l, k + 1), s = tile % kKStages;
+        if ((k >= 0 && !wait(o_done(l, h), k)) || !wait(k_full(s), tile / kKStages)) break;
+        tc_fence_after();
+        const uint32_t ka = (s * Ly::kOperand + 8192 * h) >> 4, d = tmem + 128 * l + 64 * h;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          const uint32_t off = ((e >> 2) * (kTile * 128) + 32 * (e & 3)) >> 4;
+          tc_mma_ss(d, q_lo + off, kSwz, k_lo + ka + off, kSwz, kLogit, e > 0, one);
+        }
+        if constexpr (R > 0)
+          tc_mma_ss(d, qs_lo, kFlat, ks_lo + ((s * Ly::kOperand + 1024 * h) >> 4), kFlat, kLogit, true, one);
+        tc_commit(s_full(l, h), one);
+        if (h == 1) tc_commit(k_empty(s), one);
+      }
     }
+    // the products are done before TMEM is given back
+    if (n > 0 && ok) wait(o_done(l, 1), n - 1);
     __syncwarp();
-  } else if (warp >= kDecodeWarp && warp < kMmaWarp) {
+  }
+  } else if (warp >= kDecodeWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
     const int tok = (tid - kDecodeWarp * 32) & (kTile - 1), half = (warp - kDecodeWarp) >> 2;
     float* red = reinterpret_cast<float*>(misc + 4);  // [2][8] warp maxima
     constexpr int HG = NG / 2;  // groups of this half
@@ -755,7 +748,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       const uint32_t wm = __reduce_max_sync(kAll, __float_as_uint(mx));
       if (lane == 0) red[(k & 1) * 8 + warp - kDecodeWarp] = __uint_as_float(wm);
       // one warp waits for the stage, the others for the barrier that they meet at anyway
-      if (warp == kDecodeWarp && k >= kKStages && ok && !mbar_wait_idle(k_empty(s), ((k / kKStages) - 1) & 1)) ok = false;
+      if (warp == kDecodeWarp && k >= kKStages && ok && !mbar_wait(k_empty(s), ((k / kKStages) - 1) & 1)) ok = false;
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (!tail) {  // one power of two per tile; else one per token: an unseen new token's size touches no other
         const float4 m4 = *reinterpret_cast<const float4*>(red + (k & 1) * 8);  // half 0's four have them all
@@ -836,118 +829,96 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       }
       cur = nxt;
     }
-  } else if (warp < kDecodeWarp && xb + quad * 32 < rows) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+  if (xb + (PAIR ? wl * kBlock : 0) + (warp & 3) * 32 < rows && wl < lanes_on) {
     // ---- softmax and epilogue of this warp's 32 query rows
-    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16, to = tmem_o + lane_off;
-    const int i = min(x, rows - 1) / p.G, wh = wg & 1;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + 128 * wl + lane_off, to = tmem + 256 + 128 * wl + lane_off;
+    const int i = min(x, rows - 1) / p.G;
     const float fq = t.qf[static_cast<size_t>(unit) * t.blocks * kBlock + x];
     const uint32_t* words = t.words ? t.words + (static_cast<size_t>(b) * p.span.n + i) * t.wpr : nullptr;
     const bool want_lse = p.lse != nullptr;
-    // tiles from here on hold new tokens or end the sequence
-    const int tail_at = min(P, t_hi) >= t_lo ? (min(P, t_hi) - t_lo) / kTile : 0;
-    volatile float* m_s = reinterpret_cast<volatile float*>(sm + Ly::kMax) + quad * 32 + lane;
-    volatile int* turn = reinterpret_cast<volatile int*>(sm + Ly::kTurn) + quad;
-    // The halves of the tiles are the work of four warps in turn, on one m (they share the
-    // accumulator).  Each forms its weights with the m it knows, then takes its turn (the
-    // order of the readouts anyway) to learn of the others' m and to raise it.
-    float m = -INFINITY, l = 0.0f, lx = 0.0f;
+    RowState st{-INFINITY, 0.0f, 0.0f};
+    const int nk = lane_tiles(wl);
+    // One half-tile at a time; the next one's logits are on their way while this one's
+    // weights are written.
+    uint32_t s[kHalf];
+    float f = 0.0f;
+    const int tail_at = min(P, t_hi) >= t_lo ? (min(P, t_hi) - t_lo) / kTile : 0;  // tiles from here on hold new tokens or end the sequence
 #pragma unroll 1
-    for (int k = wg >> 1; k < tiles; k += 2) {
-      const int buf = k % kLogitBufs;
-      const uint32_t sa = tmem + lane_off + kTile * buf + kHalf * wh;
-      const float* col = scale_s + (k % kRing) * kTile;
-      if (!mbar_wait_idle(s_full(buf), (k / kLogitBufs) & 1)) { ok = false; break; }
-      tc_fence_after();
-      float f = fmaxf(fq * col[0], 1e-37f);
-      if (k >= tail_at) {
-        f = fmaxf(fq, 1e-37f);
-        mask_half(sa, words, t.wpr, i, t_lo + k * kTile + kHalf * wh - P, col + kHalf * wh);
-      }
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {  // 32 tokens each, by one piece of code: the roles share the instruction cache
-        uint32_t u[32];
-        tc_ld32(sa + 32 * c, u, 0);
+    for (int y = -1; y < 2 * nk && ok; ++y) {  // step y: half y & 1 of the lane's tile y / 2
+      const int h = y & 1;
+      if (y >= 0) {
         tc_wait_ld();
-        if (!(m > -INFINITY)) m = row_max(u, f);  // (a row that has seen nothing stays at -inf)
-        uint32_t w[16], bits;
+        uint32_t w[kHalf / 2], bits;
         float sum;
-        weights32(u, f, m, w, sum, bits);
-        if (__any_sync(kAll, (bits & 0x40004000u) != 0u)) {  // a weight of 2 or more, or not a number
-          const float m2 = fmaxf(m, row_max(u, f)), a = m == m2 ? 1.0f : ex2(m - m2);
-          l *= a;
-          lx *= a;
-          if (c) l += scale_weights(sa, 16, a);
-          m = m2;
-          weights32(u, f, m, w, sum, bits);
-        }
-        l += sum;
-        if (want_lse) {  // formed once more rather than summed beside every other call's
-          const float mm = m == -INFINITY ? 0.0f : m;
+        weights(s, f, st.m, w, sum, bits);
+        // a weight of 2 or more (or not a number), or no m yet: find it, and the weights again
+        if (__any_sync(kAll, (bits & 0x40004000u) != 0u || st.m == -INFINITY)) {
+          float mx = __uint_as_float(s[0]);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) lx += ex2(fmaf(__uint_as_float(u[j]), f, -mm));
-        }
-        tc_st16(sa + 16 * c, w, 0);
-      }
-      // this half's turn: all agree on the larger m
-      if (!wait_turn(turn, 2 * k + wh)) { ok = false; break; }
-      const bool first = k == 0 && wh == 0;
-      const float known = first ? m : *m_s;
-      if (__any_sync(kAll, known != m)) {
-        const float m2 = fmaxf(known, m);
-        if (__any_sync(kAll, m2 > m)) {
-          const float a = m == -INFINITY ? 0.0f : ex2(m - m2);
-          l *= a;
-          lx *= a;
-          tc_wait_st();
-          l += scale_weights(sa, 32, a);
-        }
-        if (!first && __any_sync(kAll, m2 > known)) {
+          for (int j = 1; j < kHalf - 1; j += 2) mx = max3(mx, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+          const float top = fmaxf(mx, __uint_as_float(s[kHalf - 1])) * f;
           // the accumulator rests once the half before this one is read out
-          if (!mbar_wait(o_done(1 - wh), (wh ? k : k - 1) & 1)) ok = false;
+          if (y > 0 && !mbar_wait(o_done(wl, 1 - h), ((y - 1) >> 1) & 1)) ok = false;
           tc_fence_after();
-          scale_output<D>(to, known == -INFINITY ? 0.0f : ex2(known - m2));
+          st = raise_max<D>(st, top > st.m ? top + kSlack : st.m, to, y > 0);
+          weights(s, f, st.m, w, sum, bits);
         }
-        m = m2;
-      }
-      *m_s = m;
-      __threadfence_block();  // m before the turn
-      __syncwarp();
-      if (lane == 0) *turn = 2 * k + wh + 1;
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(buf, wh));
-    }
-    if (ok && !wait_turn(turn, 2 * tiles)) ok = false;
-    if (ok) {  // the last half's m is the row's
-      const float m2 = *m_s, a = m == m2 ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - m2);
-      l *= a;
-      lx *= a;
-      m = m2;
-    }
-    float2* sums = reinterpret_cast<float2*>(sm + Ly::kSums) + quad * 32 + lane;
-    sums[wg * kBlock] = make_float2(l, lx);
-    asm volatile("bar.sync %0, 128;" ::"r"(2 + quad) : "memory");
-    l = lx = 0.0f;
+        st.l += sum;
+        if (want_lse) {  // the unrounded weights once more, rather than their sums beside every other call's
+          const float mm = st.m == -INFINITY ? 0.0f : st.m;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      l += sums[g * kBlock].x;
-      lx += sums[g * kBlock].y;
+          for (int j = 0; j < kHalf; ++j) st.lx += ex2(fmaf(__uint_as_float(s[j]), f, -mm));
+        }
+        tc_st16(ts + kHalf * h, w, 0);
+        tc_st16(ts + kHalf * h + 16, w, 16);
+      }
+      auto hand_over = [&]() {
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(wl, h));
+      };
+      bool handed = y < 0;
+      if (y + 1 < 2 * nk) {
+        const uint32_t bar = s_full(wl, 1 - h), parity = ((y + 1) >> 1) & 1;
+        if (!__all_sync(kAll, mbar_test(bar, parity))) {  // not there yet: this one's weights first
+          if (!handed) hand_over();
+          handed = true;
+          if (!mbar_wait(bar, parity)) ok = false;
+        }
+        const int tile = tile_of(wl, (y + 1) >> 1);
+        const float* col = scale_s + (tile % kRing) * kTile;
+        const uint32_t sa = ts + kHalf * (1 - h);
+        tc_fence_after();
+        f = fmaxf(fq * col[0], 1e-37f);
+        if (tile >= tail_at) {
+          f = fmaxf(fq, 1e-37f);
+          mask_half(sa, words, t.wpr, i, t_lo + tile * kTile + kHalf * (1 - h) - P, col + kHalf * (1 - h));
+        }
+        tc_ld32(sa, s, 0);
+        tc_ld32(sa + 32, s, 32);
+      }
+      if (!handed) hand_over();
     }
-    if (ok && !mbar_wait(o_done(1), (tiles - 1) & 1)) ok = false;
+    const float m = st.m, l = st.l, lx = st.lx;
+    if (ok && nk > 0 && !mbar_wait(o_done(wl, 1), (nk - 1) & 1)) ok = false;
     tc_fence_after();
     if (ok) {
       const bool bad = *reinterpret_cast<volatile uint32_t*>(misc + 1) != 0u;
       const bool direct = p.splits == 1;
-      const size_t pr = (static_cast<size_t>(unit) * p.splits + blockIdx.y) * part_rows + x;
+      const int part = blockIdx.y * lane_parts + (PAIR ? 0 : wl);
+      const size_t pr = (static_cast<size_t>(unit) * p.splits + part) * part_rows + x;
       const int h = kv * p.G + x - i * p.G;
       const size_t orow = static_cast<size_t>(sq.row0) + i;
       const float inv = !direct ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-      constexpr int kCols = D / 4;  // each warpgroup's channels
       if (bad) {  // rare: one column at a time, in TMEM
 #pragma unroll 1
-        for (int c = wg * kCols; c < (wg + 1) * kCols; ++c) {
-          const float add = bad_values<V2>(p, words, t.wpr, i, b, kv, max(P, t_lo), t_hi, P, V2 ? channel_at(c) : c);
+        for (int c = 0; c < D; ++c) {
+          const float add = bad_values<V2, PAIR>(p, words, t.wpr, i, b, kv, max(P, t_lo), t_lo, t_hi, P, wl,
+                                                 V2 ? channel_at(c) : c);
           uint32_t w;
           asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(w) : "r"(to + c));
           tc_wait_ld();
@@ -957,27 +928,36 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         tc_wait_st();
       }
 #pragma unroll 1
-      for (int c = wg * kCols; c < (wg + 1) * kCols; c += 16) {
-        uint32_t w[16];
-        tc_ld16(to + c, w);
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t w[32];
+        tc_ld32(to + 32 * c, w, 0);
         tc_wait_ld();
-        float o[16];  // in channel order
+        float o[32];  // in channel order
 #pragma unroll
-        for (int j = 0; j < 16; ++j) o[V2 ? channel_at(j) : j] = l == 0.0f ? 0.0f : __uint_as_float(w[j]) * inv;
+        for (int j = 0; j < 32; ++j) o[V2 ? channel_at(j) : j] = __uint_as_float(w[j]);
+        if (l == 0.0f) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+        }
         if (x < rows) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 v = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-            if (direct) store_row4(p.out, orow * p.out.row_stride + h * p.out.head_stride + c + j, v);
-            else *reinterpret_cast<float4*>(p.part_o + pr * D + c + j) = v;
+          for (int j = 0; j < 32; j += 4) {
+            const float4 v = make_float4(o[j] * inv, o[j + 1] * inv, o[j + 2] * inv, o[j + 3] * inv);
+            if (direct) store_row4(p.out, orow * p.out.row_stride + h * p.out.head_stride + 32 * c + j, v);
+            else *reinterpret_cast<float4*>(p.part_o + pr * D + 32 * c + j) = v;
           }
         }
       }
-      if (wg == 0 && x < rows) {
+      if (x < rows) {
         if (!direct) p.part_ml[pr] = make_float4(m * dc::kLn2, l, lx, 0.0f);
         else if (want_lse) p.lse[orow * p.Hq + h] = l == 0.0f ? -INFINITY : m * dc::kLn2 + logf(lx);
       }
     }
+  } else if (x < rows && !PAIR && wl < lane_parts) {
+    // the lane without a tile: its split is empty
+    p.part_ml[(static_cast<size_t>(unit) * p.splits + blockIdx.y * lane_parts + wl) * part_rows + x] =
+        make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+  }
   }
 
   if (!ok) atomicOr(p.err, kDevErrWaitTimeout);
@@ -989,8 +969,8 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <int D, int R, bool V2>
-cudaError_t launch_main(const TreeParams& p, const TreeMma& t, cudaStream_t s) {
+template <int D, int R, bool V2, bool PAIR>
+cudaError_t launch_main(const TreeParams& p, const TreeMma& t, int grid_splits, cudaStream_t s) {
   CUtensorMap map{};
   if (!V2) {
     const uint64_t slabs = p.c.page_size ? static_cast<uint64_t>(p.c.num_pages) * p.c.Hkv
@@ -998,25 +978,29 @@ cudaError_t launch_main(const TreeParams& p, const TreeMma& t, cudaStream_t s) {
     const uint64_t rows = p.c.page_size ? p.c.page_size : p.c.T_cap;
     if (!encode_bf16_rows(&map, p.c.v, D, rows, slabs, 64)) return cudaErrorInvalidValue;
   }
-  auto k = tree_mma_kernel<D, R, V2>;
-  constexpr int smem = Layout<D, R>::kBytes;
+  auto k = tree_mma_kernel<D, R, V2, PAIR>;
+  constexpr int smem = Layout<D, R, V2, PAIR>::kBytes;
   static_assert(smem <= 232448, "shared memory of one CTA");
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  dim3 grid(t.blocks, p.splits, p.c.B * p.c.Hkv);
+  dim3 grid((t.blocks + (PAIR ? 1 : 0)) / (PAIR ? 2 : 1), grid_splits, p.c.B * p.c.Hkv);
   k<<<grid, kThreads, smem, s>>>(p, t, map);
   return cudaGetLastError();
 }
 
 template <int D, int R>
-cudaError_t launch_dr(const TreeParams& p, const TreeMma& t, cudaStream_t s) {
+cudaError_t launch_dr(const TreeParams& p, const TreeMma& t, int grid_splits, bool pair, cudaStream_t s) {
   const long long warps = static_cast<long long>(p.c.B) * p.c.Hkv * t.blocks * (kBlock / kPrepRows);
   const int row_ctas = static_cast<int>((warps + 7) / 8);
   const int mask_ctas = t.words ? (p.c.B * p.span.n + 7) / 8 : 0;
   tree_prep_kernel<D, R><<<row_ctas + mask_ctas, 256, 0, s>>>(p, t, row_ctas);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return p.c.vmode == HEADQ_V_2BIT ? launch_main<D, R, true>(p, t, s) : launch_main<D, R, false>(p, t, s);
+  if (p.c.vmode == HEADQ_V_2BIT)
+    return pair ? launch_main<D, R, true, true>(p, t, grid_splits, s)
+                : launch_main<D, R, true, false>(p, t, grid_splits, s);
+  return pair ? launch_main<D, R, false, true>(p, t, grid_splits, s)
+              : launch_main<D, R, false, false>(p, t, grid_splits, s);
 }
 
 }  // namespace
@@ -1028,15 +1012,15 @@ bool tree_mma_supported(const headq_cache& c) {
 
 size_t tree_mma_image_bytes(const headq_cache& c) { return operand_bytes(c.d, c.r); }
 
-cudaError_t launch_tree_mma(const TreeParams& p, const TreeMma& t, cudaStream_t s) {
+cudaError_t launch_tree_mma(const TreeParams& p, const TreeMma& t, int grid_splits, bool pair, cudaStream_t s) {
   if (p.c.d == 128) {
-    if (p.c.r == 16) return launch_dr<128, 16>(p, t, s);
-    if (p.c.r == 8) return launch_dr<128, 8>(p, t, s);
-    return launch_dr<128, 0>(p, t, s);
+    if (p.c.r == 16) return launch_dr<128, 16>(p, t, grid_splits, pair, s);
+    if (p.c.r == 8) return launch_dr<128, 8>(p, t, grid_splits, pair, s);
+    return launch_dr<128, 0>(p, t, grid_splits, pair, s);
   }
-  if (p.c.r == 16) return launch_dr<64, 16>(p, t, s);
-  if (p.c.r == 8) return launch_dr<64, 8>(p, t, s);
-  return launch_dr<64, 0>(p, t, s);
+  if (p.c.r == 16) return launch_dr<64, 16>(p, t, grid_splits, pair, s);
+  if (p.c.r == 8) return launch_dr<64, 8>(p, t, grid_splits, pair, s);
+  return launch_dr<64, 0>(p, t, grid_splits, pair, s);
 }
 
 }  // namespace headq

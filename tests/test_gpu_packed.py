@@ -305,6 +305,24 @@ def test_what_is_not_seen_is_not_felt(i, poison):
         assert not torch.isfinite(out[row]).any()
 
 
+@pytest.mark.parametrize("vmode", ["dense", "2bit"])
+@pytest.mark.parametrize("n", [100, 200, 300])
+def test_first_seen_token_late(n, vmode):
+    """Rows whose first visible token lies in a later tile than the call's first."""
+    c = Cache(21, 2, 2, 512, 128, 16, vmode)
+    rng = np.random.default_rng(n)
+    q = torch.from_numpy(rng.standard_normal((2 * n, 4, 128)).astype(np.float32)).cuda().to(BF)
+    mask = np.zeros((2, n, n), bool)
+    for i in range(n):
+        mask[:, i, i] = i % 3 > 0            # itself, or nothing
+        mask[:, i, max(0, i - 5):i] = i % 2 > 0
+    lens = [n, n]
+    cu, sl = spans([n, n], lens)
+    lse = torch.zeros(2 * n, 4, device="cuda")
+    out = hq().headq_tree_attn(c.hq, q, c.U, mask=torch.from_numpy(mask).cuda(), seq_lens=sl, cu=cu, n=n, lse=lse)
+    check_tree(out, lse, ref_tree(c, q, [n, n], lens, mask))
+
+
 def test_strided_queries_and_outputs():
     c, q, counts, lens, mask = tree_case(0, 4)
     rows, Hq, d = q.shape
