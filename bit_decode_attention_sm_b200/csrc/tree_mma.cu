@@ -696,7 +696,8 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       const int k = y >> 1, h = y & 1;
       if (k >= 0) {
         const int tile = tile_of(l, k), s = tile % VS;
-        if (!wait(p_full(l, h), k) || !wait(v_full(s), tile / VS)) break;
+        // (the values first, while the weights are not there: a wait costs some 150 cycles anyway)
+        if ((h == 0 && !wait(v_full(s), tile / VS)) || !wait(p_full(l, h), k)) break;
         tc_fence_after();
         const uint32_t va = v_lo + ((s * Ly::kVTile + 8192 * h) >> 4), w = tmem + 128 * l + 64 * h;
 #pragma unroll
@@ -707,7 +708,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       }
       if (k + 1 < n) {
         const int tile = tile_of(l, k + 1), s = tile % kKStages;
-        if ((k >= 0 && !wait(o_done(l, h), k)) || !wait(k_full(s), tile / kKStages)) break;
+        if ((h == 0 && !wait(k_full(s), tile / kKStages)) || (k >= 0 && !wait(o_done(l, h), k))) break;
         tc_fence_after();
         const uint32_t ka = (s * Ly::kOperand + 8192 * h) >> 4, d = tmem + 128 * l + 64 * h;
 #pragma unroll
