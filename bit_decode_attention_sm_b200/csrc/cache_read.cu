@@ -4,12 +4,14 @@
 // and the cached value.  fp32 arithmetic, one rounding to the output's dtype.
 //
 // Bound by HBM: a token of a KV head is 332 bytes in (d = 128, r = 16, bf16 values) and
-// 512 out.  cache_read_kernel (d 64 or 128, r 0, 8 or 16): one warp per 32-token tile of
-// one (sequence, KV head), each lane owning d/32 channels whose rows of U_h stay in its
-// registers, so a token costs r/2 broadcast loads of its side code and d*r/64 packed
-// multiply-adds per lane; codes and scales pass through the warp's shared memory once.
-// The 8 warps of a CTA take neighbouring KV heads, so that their output rows are one run
-// of memory.  Every other shape runs cache_read_any_kernel, one thread per 4 channels.
+// 512 out.  cache_read_kernel (d 64 or 128, r 0, 8 or 16): one warp per 32-token tile of one
+// (sequence, KV head).  The side code's part is a product of its small integers (exact in
+// bf16) with U_h in three bf16 parts (24 bits), tokens on the M side of mma.sync.m16n8k16,
+// summed in fp32: 12 instructions per 16 tokens x 32 channels, where packed multiply-adds
+// took 32 per token and the broadcast of the side code kept shared memory 74 % busy (344 us
+// on the 131072 x 8 tokens of the long-context layer).  The columns of the products are
+// ordered so that a lane ends with 8 neighbouring channels of its tokens: one 16-byte store
+// each in bf16.  Every other shape runs cache_read_any_kernel, one thread per 4 channels.
 #include "codec.cuh"
 
 namespace headq {
@@ -30,35 +32,35 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return r;
 }
 
-// N (2 or 4) consecutive outputs of one row
+// N (4 or 8) consecutive outputs of one row
 template <int N>
 __device__ __forceinline__ void store_out(const headq_rows& o, size_t off, const float (&x)[N]) {
   if (o.dtype == HEADQ_BF16) {
     uint32_t* p = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(o.ptr) + off);
-    if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-    else *p = pack_bf16(x[0], x[1]);
+    if constexpr (N == 8)
+      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                                pack_bf16(x[6], x[7]));
+    else *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
   } else {
-    float* p = static_cast<float*>(o.ptr) + off;
-    if constexpr (N == 4) *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    else *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(o.ptr) + off);
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) p[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
   }
 }
 
-// A warp's tile: packed codes, (minimum, scale) per group, side code entries doubled for
-// the packed multiply-add.
-template <int D, int R>
+// A warp's tile: packed codes and (minimum, scale) per group; rows a word (a pair) longer
+// than their contents, so that 8 rows read at one place fall in distinct banks.
+template <int D>
 struct WarpTile {
   static constexpr int NG = D / 32;
-  uint32_t codes[kTok][D / 16];
-  float2 ms[kTok][NG];
-  float2 w[kTok][R > 0 ? R : 1];
+  uint32_t codes[kTok][D / 16 + 1];
+  float2 ms[kTok][NG + 1];
 };
 
 // this lane's token's codes, minima and scales into the tile
-template <int D, int R>
-__device__ __forceinline__ void stage_codes(WarpTile<D, R>& t, int lane, long long row,
-                                            const uint8_t* codes, const float* scale,
-                                            const float* mn, bool groups) {
+template <int D>
+__device__ __forceinline__ void stage_codes(WarpTile<D>& t, int lane, long long row, const uint8_t* codes,
+                                            const float* scale, const float* mn, bool groups) {
   constexpr int NG = D / 32;
   uint4 c[D / 64];
   float s[NG], m[NG];
@@ -84,52 +86,86 @@ __device__ __forceinline__ void stage_codes(WarpTile<D, R>& t, int lane, long lo
       }
     }
   }
-  uint4* d = reinterpret_cast<uint4*>(t.codes[lane]);
 #pragma unroll
-  for (int k = 0; k < D / 64; ++k) d[k] = c[k];
+  for (int k = 0; k < D / 64; ++k) {
+    t.codes[lane][4 * k] = c[k].x;
+    t.codes[lane][4 * k + 1] = c[k].y;
+    t.codes[lane][4 * k + 2] = c[k].z;
+    t.codes[lane][4 * k + 3] = c[k].w;
+  }
 #pragma unroll
   for (int g = 0; g < NG; ++g) t.ms[lane][g] = make_float2(m[g], s[g]);
 }
 
-// the lane's channels of a token: min + code * scale
-template <int D, int R>
-__device__ __forceinline__ void base_values(const WarpTile<D, R>& t, int tok, int lane,
-                                            float (&x)[D / 32]) {
-  constexpr int N = D / 32;
-  const uint32_t by = reinterpret_cast<const uint8_t*>(t.codes[tok])[lane * N / 4] >> (N == 4 ? 0 : 4 * (lane & 1));
-  const float2 ms = t.ms[tok][lane * N / 32];
+// 8 codes (channels 8 q .. 8 q + 7 of group g) of a token
+template <int D>
+__device__ __forceinline__ uint32_t codes8(const WarpTile<D>& t, int tok, int g, int q) {
+  return reinterpret_cast<const uint16_t*>(t.codes[tok])[4 * g + q];
+}
+// min + code * scale of them
+template <int D>
+__device__ __forceinline__ void base8(const WarpTile<D>& t, int tok, int g, int q, float (&x)[8]) {
+  const uint32_t c = codes8<D>(t, tok, g, q);
+  const float2 ms = t.ms[tok][g];
 #pragma unroll
-  for (int k = 0; k < N; ++k) x[k] = fmaf(code_f(by >> (2 * k)), ms.y, ms.x);
+  for (int k = 0; k < 8; ++k) x[k] = fmaf(code_f(c >> (2 * k)), ms.y, ms.x);
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// entries 2t, 2t + 1 of a side code (one byte) as bf16
+__device__ __forceinline__ uint32_t side_pair(uint32_t byte) {
+  const float a = __uint_as_float((byte & 15u) ^ 0x4B000008u) - 8388616.0f;  // nibble ^ 8 is w + 8
+  const float b = __uint_as_float(((byte >> 4) & 15u) ^ 0x4B000008u) - 8388616.0f;
+  return pack_bf16(a, b);
 }
 
 template <int D, int R, bool KCH>
 __global__ void __launch_bounds__(kWarps * 32, 2)
 cache_read_kernel(const headq_cache c, const headq_span span, const float* U, float sigma,
-                  const headq_rows ko, const headq_rows vo, unsigned* err, int tiles, int sub) {
-  constexpr int N = D / 32;
-  extern __shared__ uint4 smem[];
-  using Tile = WarpTile<D, R>;
-  Tile& t = reinterpret_cast<Tile*>(smem)[threadIdx.x >> 5];
-  const int lane = threadIdx.x & 31;
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int kv = static_cast<int>(unit % c.Hkv);
-  const long long bt = unit / c.Hkv;
-  const int b = static_cast<int>(bt / tiles);
-  if (b >= c.B) return;
-  const int i0 = static_cast<int>(bt % tiles) * kTok * sub;
+                  const headq_rows ko, const headq_rows vo, unsigned* err, int blocks, int sub) {
+  constexpr int NG = D / 32;
+  using Tile = WarpTile<D>;
+  __shared__ Tile tiles[kWarps];
+  __shared__ uint2 u_s[R > 0 ? NG * 4 * 3 * 32 : 1];  // [group][n-tile][part][lane]
+  Tile& t = tiles[threadIdx.x >> 5];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int kv = blockIdx.x % c.Hkv;
+  const int bt = blockIdx.x / c.Hkv, b = bt / blocks;
+  const int i0 = ((bt - b * blocks) * kWarps + warp) * kTok * sub;
   const SpanSeq sq = span_seq(span, b);
-  if (sq.p0 < 0 || i0 >= sq.n) return;
+  if (sq.p0 < 0 || (bt - b * blocks) * kWarps * kTok * sub >= sq.n) return;
+  const int gq = lane >> 2, tq = lane & 3;  // a lane's tokens gq, gq + 8 and channels 8 tq .. of a group
 
-  uint64_t u[R > 0 ? R : 1][N / 2];  // (channel pair) of each basis vector
   if constexpr (R > 0) {
     if (ko.ptr) {
-      const float* up = U + (static_cast<size_t>(kv) * D + lane * N) * R;
+      // n-tile j's column 2 t + e is channel 8 t + 2 j + e of its group; parts of U from the
+      // leading one down
+      for (int e = threadIdx.x; e < NG * 4 * 32; e += kWarps * 32) {
+        const int ln = e & 31, j = (e >> 5) & 3, g = e >> 7;
+        const int col = ln >> 2, ch = 32 * g + 8 * (col >> 1) + 2 * j + (col & 1), k0 = 2 * (ln & 3);
+        const float* up = U + (static_cast<size_t>(kv) * D + ch) * R;
+        float x[4] = {__ldg(up + k0), __ldg(up + k0 + 1), 0.0f, 0.0f};
+        if (R > 8) {
+          x[2] = __ldg(up + k0 + 8);
+          x[3] = __ldg(up + k0 + 9);
+        }
 #pragma unroll
-      for (int k = 0; k < N / 2; ++k)
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-          u[i][k] = codec::pk2(__ldg(up + 2 * k * R + i), __ldg(up + (2 * k + 1) * R + i));
+        for (int part = 0; part < 3; ++part) {
+          const uint32_t lo = pack_bf16(x[0], x[1]), hi = pack_bf16(x[2], x[3]);
+          u_s[((g * 4 + j) * 3 + part) * 32 + ln] = make_uint2(lo, hi);
+          x[0] -= __uint_as_float(lo << 16);
+          x[1] -= __uint_as_float(lo & 0xffff0000u);
+          x[2] -= __uint_as_float(hi << 16);
+          x[3] -= __uint_as_float(hi & 0xffff0000u);
+        }
+      }
     }
+    __syncthreads();
   }
 
   for (int s = 0; s < sub; ++s) {
@@ -144,77 +180,98 @@ cache_read_kernel(const headq_cache c, const headq_span span, const float* U, fl
     const size_t out0 = static_cast<size_t>(sq.row0) + i1;
     if (ko.ptr) {
       __syncwarp();
-      stage_codes<D, R>(t, lane, row, c.k_codes, c.k_scale, c.k_min, !KCH);
+      stage_codes<D>(t, lane, row, c.k_codes, c.k_scale, c.k_min, !KCH);
+      uint32_t zc[R > 0 ? R / 8 : 1];
+      float zs = 0.0f;
       if constexpr (R > 0) {
-        uint32_t zc[R / 8];
-        float zs = 0.0f;
 #pragma unroll
-        for (int k = 0; k < R / 8; ++k) zc[k] = 0u;
+        for (int k = 0; k < R / 8; ++k) zc[k] = 0x00000000u;
         if (row >= 0) {
           const uint32_t* zp = reinterpret_cast<const uint32_t*>(c.z_codes + row * (R / 2));
 #pragma unroll
           for (int k = 0; k < R / 8; ++k) zc[k] = __ldg(zp + k);
           zs = sigma * __ldg(c.z_scale + row);
         }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          // nibble ^ 8 is w + 8 for a two's-complement nibble w
-          const uint32_t nb = ((zc[i / 8] >> (4 * (i % 8))) & 15u) ^ 8u;
-          const float w = (__uint_as_float(0x4B000000u | nb) - 8388616.0f) * zs;
-          t.w[lane][i] = make_float2(w, w);
-        }
       }
       __syncwarp();
-#pragma unroll 2
-      for (int tok = 0; tok < nt; ++tok) {
-        float x[N];
-        if constexpr (KCH) {
-          const long long rt = __shfl_sync(kFull, row, tok);
-#pragma unroll
-          for (int k = 0; k < N; ++k) x[k] = 0.0f;
-          if (rt >= 0) {
-            const uint32_t by = reinterpret_cast<const uint8_t*>(t.codes[tok])[lane * N / 4] >> (N == 4 ? 0 : 4 * (lane & 1));
-            const float* sc = c.k_scale + (rt >> 6) * D + lane * N;
-            const float* mn = c.k_min + (rt >> 6) * D + lane * N;
-#pragma unroll
-            for (int k = 0; k < N; ++k) x[k] = fmaf(code_f(by >> (2 * k)), __ldg(sc + k), __ldg(mn + k));
-          }
-        } else {
-          base_values<D, R>(t, tok, lane, x);
-        }
+#pragma unroll 1
+      for (int mt = 0; mt < 2 && 16 * mt < nt; ++mt) {
+        uint32_t a[4] = {0, 0, 0, 0};
+        float zt[2] = {0.0f, 0.0f};
         if constexpr (R > 0) {
-          uint64_t a[N / 2];
 #pragma unroll
-          for (int k = 0; k < N / 2; ++k) a[k] = codec::pk2(x[2 * k], x[2 * k + 1]);
-          const ulonglong2* wp = reinterpret_cast<const ulonglong2*>(t.w[tok]);
-#pragma unroll
-          for (int i = 0; i < R; i += 2) {
-            const ulonglong2 w2 = wp[i / 2];
-#pragma unroll
-            for (int k = 0; k < N / 2; ++k) {
-              a[k] = codec::fma2(u[i][k], w2.x, a[k]);
-              a[k] = codec::fma2(u[i + 1][k], w2.y, a[k]);
+          for (int e = 0; e < 2; ++e) {
+            const int tok = 16 * mt + gq + 8 * e;
+            const uint32_t lo = __shfl_sync(kFull, zc[0], tok);
+            a[e] = side_pair((lo >> (8 * tq)) & 255u);
+            if constexpr (R > 8) {
+              const uint32_t hi = __shfl_sync(kFull, zc[1], tok);
+              a[2 + e] = side_pair((hi >> (8 * tq)) & 255u);
             }
-          }
-#pragma unroll
-          for (int k = 0; k < N / 2; ++k) {
-            x[2 * k] = codec::pk_lo(a[k]);
-            x[2 * k + 1] = codec::pk_hi(a[k]);
+            zt[e] = __shfl_sync(kFull, zs, tok);
           }
         }
-        store_out<N>(ko, (out0 + tok) * ko.row_stride + kv * ko.head_stride + lane * N, x);
+        long long rt[2] = {0, 0};
+        if constexpr (KCH) {
+          rt[0] = __shfl_sync(kFull, row, 16 * mt + gq);
+          rt[1] = __shfl_sync(kFull, row, 16 * mt + gq + 8);
+        }
+#pragma unroll 2
+        for (int g = 0; g < NG; ++g) {
+          float acc[4][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+          if constexpr (R > 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int part = 2; part >= 0; --part) {  // the small parts first
+                const uint2 bu = u_s[((g * 4 + j) * 3 + part) * 32 + lane];
+                mma_bf16(acc[j], a, bu.x, bu.y);
+              }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int tok = 16 * mt + gq + 8 * e;
+            float x[8];
+            if constexpr (KCH) {
+              const uint32_t cb = codes8<D>(t, tok, g, tq);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[k] = 0.0f;
+              if (rt[e] >= 0) {
+                const size_t o = static_cast<size_t>(rt[e] >> 6) * D + 32 * g + 8 * tq;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = fmaf(code_f(cb >> (2 * k)), __ldg(c.k_scale + o + k), __ldg(c.k_min + o + k));
+              }
+            } else {
+              base8<D>(t, tok, g, tq, x);
+            }
+            if constexpr (R > 0) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                x[2 * j] = fmaf(acc[j][2 * e], zt[e], x[2 * j]);
+                x[2 * j + 1] = fmaf(acc[j][2 * e + 1], zt[e], x[2 * j + 1]);
+              }
+            }
+            if (tok < nt) store_out<8>(ko, (out0 + tok) * ko.row_stride + kv * ko.head_stride + 32 * g + 8 * tq, x);
+          }
+        }
       }
     }
     if (!vo.ptr) continue;
     if (c.vmode == HEADQ_V_2BIT) {
       __syncwarp();
-      stage_codes<D, R>(t, lane, row, c.v_codes, c.v_scale, c.v_min, true);
+      stage_codes<D>(t, lane, row, c.v_codes, c.v_scale, c.v_min, true);
       __syncwarp();
-#pragma unroll 2
-      for (int tok = 0; tok < nt; ++tok) {
-        float x[N];
-        base_values<D, R>(t, tok, lane, x);
-        store_out<N>(vo, (out0 + tok) * vo.row_stride + kv * vo.head_stride + lane * N, x);
+      for (int tok = gq; tok < nt; tok += 8) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          float x[8];
+          base8<D>(t, tok, g, tq, x);
+          store_out<8>(vo, (out0 + tok) * vo.row_stride + kv * vo.head_stride + 32 * g + 8 * tq, x);
+        }
       }
     } else if (c.v_dtype == HEADQ_BF16 && vo.dtype == HEADQ_BF16) {  // the same bits
       constexpr int CPR = D / 8;        // 16-byte chunks per row
@@ -242,11 +299,11 @@ cache_read_kernel(const headq_cache c, const headq_span span, const float* U, fl
       const bool vb = c.v_dtype == HEADQ_BF16;
       for (int tok = 0; tok < nt; ++tok) {
         const long long rt = __shfl_sync(kFull, row, tok);
-        float x[N];
+        if (lane >= D / 4) continue;
+        float x[4];
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-          x[k] = rt < 0 ? 0.0f : load_elem(c.v, rt * D + lane * N + k, vb);
-        store_out<N>(vo, (out0 + tok) * vo.row_stride + kv * vo.head_stride + lane * N, x);
+        for (int k = 0; k < 4; ++k) x[k] = rt < 0 ? 0.0f : load_elem(c.v, rt * D + lane * 4 + k, vb);
+        store_out<4>(vo, (out0 + tok) * vo.row_stride + kv * vo.head_stride + lane * 4, x);
       }
     }
   }
@@ -308,21 +365,15 @@ cache_read_any_kernel(const headq_cache c, const headq_span span, const float* U
 
 template <int D, int R>
 cudaError_t launch_fast(const CacheReadParams& p, cudaStream_t s) {
-  // Tokens per warp: 2 tiles once that leaves several warps for every slot of the GPU (a
-  // warp's registers of U_h are then read half as often), else 1.
+  // Tiles per warp: 2 once that leaves several waves of warps (U_h is then split half as
+  // often), else 1.
   const long long warps = static_cast<long long>(p.c.B) * p.c.Hkv * ((p.span.n + kTok - 1) / kTok);
-  const int sub = warps >= 8ll * 32 * sm_count() / 2 ? 2 : 1;
-  const int tiles = (p.span.n + kTok * sub - 1) / (kTok * sub);
-  const long long units = static_cast<long long>(p.c.B) * p.c.Hkv * tiles;
+  const int sub = warps >= 4ll * 16 * sm_count() ? 2 : 1;
+  const int per = kTok * sub * kWarps, blocks = (p.span.n + per - 1) / per;
+  const long long grid = static_cast<long long>(p.c.B) * p.c.Hkv * blocks;
   auto k = p.c.kmode == HEADQ_K_CHANNEL ? cache_read_kernel<D, R, true> : cache_read_kernel<D, R, false>;
-  const size_t smem = kWarps * sizeof(WarpTile<D, R>);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  const long long grid = (units + kWarps - 1) / kWarps;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  k<<<static_cast<unsigned>(grid), kWarps * 32, smem, s>>>(p.c, p.span, p.U, p.sigma, p.k, p.v, p.err, tiles, sub);
+  k<<<static_cast<unsigned>(grid), kWarps * 32, 0, s>>>(p.c, p.span, p.U, p.sigma, p.k, p.v, p.err, blocks, sub);
   return cudaGetLastError();
 }
 
