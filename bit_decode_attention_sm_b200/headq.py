@@ -539,13 +539,30 @@ def headq_a2_value_fixup(cache, q, U, keep_idx, keep_v, out, lse, T=None, seq_le
     return out
 
 
-def _same_device(cache, **tensors):
-    """The cache's device, on which every tensor of a call must be."""
-    dev = cache.k_codes.device
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError("%s is on %s, the cache on %s" % (name, t.device, dev))
+# The packed-batch calls are made once per layer and step, often on work of a few
+# microseconds: their argument handling below keeps to plain integers, and enters a device
+# guard only when the cache is on another device than the current one.
+
+def _same_device(cache, tensors):
+    """The index of the cache's device, on which every tensor of a call must be."""
+    dev = cache.k_codes.get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("a tensor is on %s, the cache on %s" % (t.device, cache.k_codes.device))
     return dev
+
+
+def _call(name, dev, stream, *args):
+    """Entry point `name` on device `dev` and its current stream (or `stream`)."""
+    fn = getattr(_lib or lib(), name)
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st != 0:
+        raise HeadQError(name, st)
 
 
 def _rows(t, name, heads, d, written=False):
@@ -602,10 +619,6 @@ def _basis(cache, U):
     return U.data_ptr()
 
 
-def _stream_on(dev, stream):
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
-
-
 def headq_cache_write_ragged(cache, k, v, U, seq_lens=None, cu=None, n=None, T=None, src=None,
                              stream=None):
     """Encode a packed batch of new tokens, k and v [rows, Hkv, d] (v None: values left as
@@ -620,13 +633,10 @@ def headq_cache_write_ragged(cache, k, v, U, seq_lens=None, cu=None, n=None, T=N
     if v is not None and (v.dtype != k.dtype or v.shape[0] != k.shape[0]):
         raise ValueError("k and v must have the same dtype and rows")
     rows = k.shape[0] if src is None else src.shape[0]
-    dev = _same_device(cache, k=k, v=v, U=U, seq_lens=seq_lens, cu=cu, src=src)
+    dev = _same_device(cache, (k, v, U, seq_lens, cu, src))
     sp = _span(cache, seq_lens, cu, n, T, rows)
-    cs = cache.struct()
-    with torch.cuda.device(dev):
-        _check("headq_cache_write_ragged", lib().headq_cache_write_ragged(
-            cs, ks, vs, k.shape[0], _int32(src, "src", (rows,)), sp, _basis(cache, U),
-            _stream_on(dev, stream)))
+    _call("headq_cache_write_ragged", dev, stream, cache.struct(), ks, vs, k.shape[0],
+          _int32(src, "src", (rows,)), sp, _basis(cache, U))
 
 
 def headq_cache_read(cache, U, seq_lens=None, cu=None, n=None, T=None, rows=None, corr_sign=1,
@@ -649,13 +659,10 @@ def headq_cache_read(cache, U, seq_lens=None, cu=None, n=None, T=None, rows=None
         raise ValueError("k_out and v_out must have the same rows")
     ks = None if k_out is None else _rows(k_out, "k_out", cache.Hkv, cache.d, True)
     vs = None if v_out is None else _rows(v_out, "v_out", cache.Hkv, cache.d, True)
-    dev = _same_device(cache, k_out=k_out, v_out=v_out, U=U, seq_lens=seq_lens, cu=cu, ws=ws)
+    dev = _same_device(cache, (k_out, v_out, U, seq_lens, cu, ws))
     sp = _span(cache, seq_lens, cu, n, T, have[0])
-    cs = cache.struct()
-    with torch.cuda.device(dev):
-        _check("headq_cache_read", lib().headq_cache_read(
-            cs, sp, None if k_out is None else _basis(cache, U), int(corr_sign), ks, vs,
-            None if ws is None else ws.data_ptr(), _stream_on(dev, stream)))
+    _call("headq_cache_read", dev, stream, cache.struct(), sp, None if k_out is None else _basis(cache, U),
+          int(corr_sign), ks, vs, None if ws is None else ws.data_ptr())
     return k_out, v_out
 
 
@@ -689,7 +696,7 @@ def headq_tree_attn(cache, q, U, mask=None, seq_lens=None, cu=None, n=None, T=No
         raise ValueError("out must have q's rows and dtype")
     if lse is not None and (_cuda(lse, "lse").dtype != torch.float32 or tuple(lse.shape) != (rows, Hq)):
         raise ValueError("lse must be float32 [%d, %d]" % (rows, Hq))
-    dev = _same_device(cache, q=q, out=out, U=U, mask=mask, seq_lens=seq_lens, cu=cu, lse=lse, ws=ws)
+    dev = _same_device(cache, (q, out, U, mask, seq_lens, cu, lse, ws))
     sp = _span(cache, seq_lens, cu, n, T, rows)
     mp, ms = None, 0
     if mask is not None:
@@ -703,12 +710,8 @@ def headq_tree_attn(cache, q, U, mask=None, seq_lens=None, cu=None, n=None, T=No
     if ws is None:
         ws = tree_workspace(cache, Hq, sp.n, sp.T)
     sm = 1.0 / math.sqrt(cache.d) if sm_scale is None else float(sm_scale)
-    cs = cache.struct()
-    with torch.cuda.device(dev):
-        _check("headq_tree_attn", lib().headq_tree_attn(
-            cs, qs, Hq, mp, ms, sp, _basis(cache, U), sm, int(corr_sign), os_,
-            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
-            _stream_on(dev, stream)))
+    _call("headq_tree_attn", dev, stream, cache.struct(), qs, Hq, mp, ms, sp, _basis(cache, U), sm,
+          int(corr_sign), os_, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
