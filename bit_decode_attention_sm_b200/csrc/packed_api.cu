@@ -1,5 +1,7 @@
 // C ABI of the packed-batch entry points (headq_span, headq_rows): argument checks and
 // launches of headq_cache_write_ragged, headq_cache_read and headq_tree_attn.
+#include <algorithm>
+
 #include "headq_internal.cuh"
 #include "tree.cuh"
 
@@ -32,15 +34,40 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 struct TreeWs {
   size_t part_ml, qimg, qf, words, bytes;
 };
-TreeWs tree_ws(const headq_cache& c, int Hq, int n, const TreePlan& tp) {
+TreeWs tree_ws(const headq_cache& c, int n, size_t part_rows, bool mma, int blocks) {
   TreeWs w{};
   const size_t units = static_cast<size_t>(c.B) * c.Hkv;
-  const size_t rows = tp.parts > 1 ? static_cast<size_t>(c.B) * Hq * n * tp.parts : 0;
-  w.part_ml = kWsHeaderBytes + round256(rows * c.d * sizeof(float));
-  w.qimg = w.part_ml + round256(rows * sizeof(float4));
-  w.qf = w.qimg + (tp.mma ? round256(units * tp.blocks * tree_mma_image_bytes(c)) : 0);
-  w.words = w.qf + (tp.mma ? round256(units * tp.blocks * 128 * sizeof(float)) : 0);
-  w.bytes = w.words + (tp.mma ? round256(static_cast<size_t>(c.B) * n * ((n + 31) / 32) * 4) : 0);
+  w.part_ml = kWsHeaderBytes + round256(part_rows * c.d * sizeof(float));
+  w.qimg = w.part_ml + round256(part_rows * sizeof(float4));
+  w.qf = w.qimg + (mma ? round256(units * blocks * tree_mma_image_bytes(c)) : 0);
+  w.words = w.qf + (mma ? round256(units * blocks * 128 * sizeof(float)) : 0);
+  w.bytes = w.words + (mma ? round256(static_cast<size_t>(c.B) * n * ((n + 31) / 32) * 4) : 0);
+  return w;
+}
+
+// most splits of decode_plan for any length up to T
+int decode_max_splits(const headq_cache& c, int Hq, int T) {
+  const int units = c.B * c.Hkv, G = Hq / c.Hkv;
+  if (units <= 0 || !mma_decode_supported(c, G)) return 0;
+  const int slots = mma_decode_ctas_per_sm(c, G) * sm_count();
+  return std::max(1, std::min({(T + 63) / 64, kMaxMmaSplits, 4 * ((slots + units - 1) / units) + 4}));
+}
+
+// ... and of single tokens: [error word][queries][lengths][outputs][log-sum-exps][arrival
+// counters, zeroed by each call][partials of the decode kernel]
+struct TreeOneWs {
+  size_t q, lens, out, lse, counters, part, bytes;
+};
+TreeOneWs tree_one_ws(const headq_cache& c, int Hq, int splits) {
+  TreeOneWs w{};
+  const size_t rows = static_cast<size_t>(c.B) * Hq;
+  w.q = kWsHeaderBytes;
+  w.lens = w.q + round256(rows * c.d * 2);
+  w.out = w.lens + round256(static_cast<size_t>(c.B) * 4);
+  w.lse = w.out + round256(rows * c.d * 4);
+  w.counters = w.lse + round256(rows * 4);
+  w.part = w.counters + round256(static_cast<size_t>(c.B) * c.Hkv * 4);
+  w.bytes = w.part + round256(rows * splits * (c.d + 2) * sizeof(float));
   return w;
 }
 
@@ -110,9 +137,13 @@ HEADQ_API headq_status headq_cache_read(const headq_cache* cache, const headq_sp
 
 HEADQ_API size_t headq_tree_workspace_bytes(const headq_cache* cache, int Hq, int n, int T) {
   if (check_cache(cache) != HEADQ_OK || Hq <= 0 || Hq % cache->Hkv || n < 0 || T < 0) return 0;
-  const size_t a = tree_ws(*cache, Hq, n, tree_plan(*cache, Hq, n, T, true)).bytes;
-  const size_t b = tree_ws(*cache, Hq, n, tree_plan(*cache, Hq, n, T, false)).bytes;
-  return a > b ? a : b;  // the queries' dtype is not known here
+  // the largest over both dtypes of the queries and every smaller n and T
+  size_t most = tree_ws(*cache, n, tree_max_part_rows(*cache, Hq, n, T, false), false, 0).bytes;
+  if (!tree_mma_supported(*cache) || cache->B == 0) return most;
+  const long long blocks = (static_cast<long long>(n) * (Hq / cache->Hkv) + 127) / 128;
+  most = std::max(most, tree_ws(*cache, n, tree_max_part_rows(*cache, Hq, n, T, true), true,
+                                static_cast<int>(blocks)).bytes);
+  return std::max(most, tree_one_ws(*cache, Hq, decode_max_splits(*cache, Hq, T)).bytes);
 }
 
 HEADQ_API headq_status headq_tree_attn(const headq_cache* cache, const headq_rows* q, int Hq,
@@ -137,8 +168,11 @@ HEADQ_API headq_status headq_tree_attn(const headq_cache* cache, const headq_row
   if (cache->r > 0 && (!U || !aligned16(U))) return HEADQ_ERR_INVALID_ARG;
   const bool qb = q->dtype == HEADQ_BF16;
   const TreePlan tp = tree_plan(*cache, Hq, span->n, span->T, qb);
-  const TreeWs w = tree_ws(*cache, Hq, span->n, tp);
-  if (!ws || !aligned16(ws) || ws_bytes < w.bytes) return HEADQ_ERR_WORKSPACE;
+  const size_t part_rows =
+      tp.parts > 1 ? static_cast<size_t>(cache->B) * Hq * span->n * tp.parts : 0;
+  const TreeWs w = tree_ws(*cache, span->n, part_rows, tp.mma, tp.blocks);
+  const TreeOneWs o = tree_one_ws(*cache, Hq, tp.one ? decode_plan(*cache, Hq, span->T).splits : 0);
+  if (!ws || !aligned16(ws) || ws_bytes < (tp.one ? o.bytes : w.bytes)) return HEADQ_ERR_WORKSPACE;
   TreeParams p{};
   p.c = *cache;
   p.q = *q;
@@ -156,6 +190,16 @@ HEADQ_API headq_status headq_tree_attn(const headq_cache* cache, const headq_row
   p.chunk = tp.chunk;
   uint8_t* base = static_cast<uint8_t*>(ws);
   p.err = reinterpret_cast<unsigned*>(base);
+  if (tp.one) {
+    const TreeOne t{base + o.q,
+                    reinterpret_cast<int32_t*>(base + o.lens),
+                    reinterpret_cast<float*>(base + o.out),
+                    reinterpret_cast<float*>(base + o.lse),
+                    reinterpret_cast<unsigned*>(base + o.counters),
+                    reinterpret_cast<float*>(base + o.part)};
+    return launch_tree_one(p, t, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? HEADQ_OK
+                                                                                        : HEADQ_ERR_CUDA;
+  }
   p.part_o = reinterpret_cast<float*>(base + kWsHeaderBytes);
   p.part_ml = reinterpret_cast<float4*>(base + w.part_ml);
   TreeMma t{};

@@ -5,14 +5,29 @@
 
 namespace headq {
 
-// How a call runs: on the tensor cores (tree_mma.cu) with one or (pair) two 128-row blocks
-// per CTA, or in fp32 (tree_attn.cu); grid_splits T-splits of `chunk` tokens per (sequence,
-// KV head), which leave `parts` partial results to merge (1: none).
+// How a call runs: single tokens on the decode kernels (one), on the tensor cores
+// (tree_mma.cu) with one or (pair) two 128-row blocks per CTA, or in fp32 (tree_attn.cu);
+// grid_splits T-splits of `chunk` tokens per (sequence, KV head), which leave `parts` partial
+// results to merge (1: none).
 struct TreePlan {
-  bool mma, pair;
+  bool one, mma, pair;
   int blocks, grid_splits, parts, chunk;
 };
 TreePlan tree_plan(const headq_cache& c, int Hq, int n, int T, bool q_bf16);
+// most partial results (query rows x parts) of any call with up to n new tokens per sequence
+// and up to T cached ones, on the tensor cores and in fp32
+size_t tree_max_part_rows(const headq_cache& c, int Hq, int n, int T, bool mma);
+
+// Single tokens: the decode kernels' contiguous queries, lengths, outputs and log-sum-exps in
+// the workspace.
+struct TreeOne {
+  void* q;
+  int32_t* lens;
+  float *out, *lse;
+  unsigned* counters;
+  float* part;
+};
+cudaError_t launch_tree_one(const TreeParams& p, const TreeOne& w, cudaStream_t s);
 
 // Operands of the tensor-core kernel in the workspace: shared-memory images of the query
 // rows [unit][block], each row's logit factor [unit][block * 128], mask bits [B][n][wpr]

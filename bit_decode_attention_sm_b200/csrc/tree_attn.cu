@@ -14,6 +14,8 @@
 // take.
 #include <math.h>
 
+#include <algorithm>
+
 #include "codec.cuh"
 #include "tree.cuh"
 
@@ -264,6 +266,43 @@ tree_merge_kernel(const TreeParams p) {
   if (p.lse && lane == 0) p.lse[orow * p.Hq + kv * p.G + g] = L == 0.0f ? -INFINITY : M + logf(Lx);
 }
 
+// Single tokens on the decode kernels: the queries gathered to [B, Hq, d], and the tokens each
+// sequence's query sees -- the first p0, and itself unless its mask entry is 0.
+__global__ void __launch_bounds__(256)
+tree_one_prep_kernel(const TreeParams p, const TreeOne w) {
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const SpanSeq sq = span_seq(p.span, b);
+  const bool part = sq.n > 0 && sq.p0 >= 0;
+  if (tid == 0) w.lens[b] = part ? sq.p0 + (tree_sees(p, b, 0, 0) ? 1 : 0) : 0;
+  for (int h = tid; h < p.c.Hkv; h += 256) w.counters[b * p.c.Hkv + h] = 0u;
+  const int per = p.c.d / 8;  // 16-byte pieces of a bf16 row
+  for (int e = tid; e < p.Hq * per; e += 256) {
+    const int h = e / per, c = e - h * per;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (part)
+      x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.ptr) + sq.row0 * p.q.row_stride +
+                                          h * p.q.head_stride + 8 * c);
+    static_cast<uint4*>(w.q)[static_cast<size_t>(b) * p.Hq * per + e] = x;
+  }
+}
+
+// their results to the packed rows
+__global__ void __launch_bounds__(256)
+tree_one_finish_kernel(const TreeParams p, const TreeOne w) {
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const SpanSeq sq = span_seq(p.span, b);
+  if (sq.n == 0) return;
+  const int per = p.c.d / 4;
+  for (int e = tid; e < p.Hq * per; e += 256) {
+    const int h = e / per, c4 = e - h * per;
+    store_row4(p.out, sq.row0 * p.out.row_stride + h * p.out.head_stride + 4 * c4,
+               reinterpret_cast<const float4*>(w.out)[static_cast<size_t>(b) * p.Hq * per + e]);
+  }
+  if (p.lse)
+    for (int h = tid; h < p.Hq; h += 256)
+      p.lse[static_cast<size_t>(sq.row0) * p.Hq + h] = w.lse[static_cast<size_t>(b) * p.Hq + h];
+}
+
 template <int D>
 cudaError_t launch_any(const TreeParams& p, cudaStream_t s) {
   const int rc = row_chunks(D, p.c.r);
@@ -287,20 +326,29 @@ cudaError_t launch_merge(const TreeParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// Tensor cores: one CTA per SM, so the splits that minimise waves x (tiles per CTA + 3),
-// the 3 standing for a CTA's set-up, first loads and epilogue.  fp32 kernel: about four
-// CTAs per SM, chunks of whole 32-token tiles.
+// Single tokens: the decode kernels where they use the tensor cores; a 128-row tile of which
+// Hq / Hkv <= 8 rows are live waits longer on each step (69 us against 44 at 16 sequences of
+// up to 8192 tokens, 28 heads on 4).  Tensor cores: one CTA per SM, so the splits that minimise
+// waves x (tiles per CTA + 3), the 3 standing for a CTA's set-up, first loads and epilogue;
+// at most kMaxWaves waves, which bounds the workspace.  fp32 kernel: about four CTAs per SM,
+// chunks of whole 32-token tiles.
+constexpr long long kMaxWaves = 8;
+
 TreePlan tree_plan(const headq_cache& c, int Hq, int n, int T, bool q_bf16) {
   const long long units = static_cast<long long>(c.B) * c.Hkv, rows = static_cast<long long>(n) * (Hq / c.Hkv);
-  TreePlan tp{q_bf16 && tree_mma_supported(c), false, static_cast<int>((rows + 127) / 128), 1, 1, 128};
+  TreePlan tp{false, q_bf16 && tree_mma_supported(c), false, static_cast<int>((rows + 127) / 128), 1, 1, 128};
   if (n <= 0 || units <= 0) return tp;
   const int sms = sm_count();
+  if (tp.mma && n == 1 && units <= kMaxFusedUnits && decode_plan(c, Hq, T).mma) {
+    tp.one = true;
+    return tp;
+  }
   if (tp.mma) {
     tp.pair = tp.blocks > 1;
     const long long ctas = units * (tp.pair ? (tp.blocks + 1) / 2 : tp.blocks);
     const int tiles = T > 128 ? (T + 127) / 128 : 1;
     long long best = -1;
-    for (int s = 1; s <= tiles && s <= sms; ++s) {
+    for (int s = 1; s <= tiles && s <= sms && (s == 1 || ctas * s <= kMaxWaves * sms); ++s) {
       const int per = (tiles + s - 1) / s, used = (tiles + per - 1) / per;
       if (used != s) continue;
       const long long cost = ((ctas * s + sms - 1) / sms) * (per + 3) + (s > 1 ? 1 : 0);
@@ -322,6 +370,48 @@ TreePlan tree_plan(const headq_cache& c, int Hq, int n, int T, bool q_bf16) {
   tp.chunk = per * kTT;
   tp.grid_splits = tp.parts = (tiles + per - 1) / per;
   return tp;
+}
+
+// A call's splits are not monotone in its sizes, so the bound comes from what limits them:
+// at least `units` CTAs a split, the caps on the grid above, and whole tiles; and a grid of
+// C CTAs holds at most C x (rows of a CTA) x (parts of a CTA) partial rows.
+size_t tree_max_part_rows(const headq_cache& c, int Hq, int n, int T, bool mma) {
+  const long long units = static_cast<long long>(c.B) * c.Hkv, rows = units * n * (Hq / c.Hkv);
+  if (rows <= 0) return 0;
+  const long long grid = (mma ? kMaxWaves : 4) * sm_count(), tile = mma ? 128 : kTT;
+  const long long tiles = T > tile ? (T + tile - 1) / tile : 1;
+  const long long splits = std::min<long long>({tiles, std::max(1ll, grid / units), mma ? sm_count() : 64ll});
+  return static_cast<size_t>(mma ? std::min(rows * 2 * splits, 256 * std::max(grid, units))
+                                 : std::min(rows * splits, kRT * grid));
+}
+
+cudaError_t launch_tree_one(const TreeParams& p, const TreeOne& w, cudaStream_t s) {
+  tree_one_prep_kernel<<<p.c.B, 256, 0, s>>>(p, w);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const DecodePlan dp = decode_plan(p.c, p.Hq, p.span.T);
+  DecodeParams d{};
+  d.c = p.c;
+  d.q = w.q;
+  d.q_bf16 = true;
+  d.Hq = p.Hq;
+  d.G = p.G;
+  d.T = p.span.T;
+  d.seq_lens = w.lens;
+  d.U = p.U;
+  d.sm_scale = p.sm_scale;
+  d.corr_sign = p.corr_sign;
+  d.splits = dp.splits;
+  d.chunk = dp.chunk;
+  d.err = p.err;
+  d.counters = w.counters;
+  d.fused = dp.fused;
+  d.part = w.part;
+  d.out = w.out;
+  d.lse = w.lse;
+  if ((e = launch_decode(d, dp.mma, s)) != cudaSuccess) return e;
+  tree_one_finish_kernel<<<p.c.B, 256, 0, s>>>(p, w);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_tree(const TreeParams& p, const TreeMma& t, const TreePlan& plan, cudaStream_t s) {

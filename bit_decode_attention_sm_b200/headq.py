@@ -13,6 +13,7 @@ Names follow the C ABI: :func:`headq_calibrate`, :func:`headq_cache_write`,
 planes.
 """
 
+import contextlib
 import ctypes
 import math
 import os
@@ -555,6 +556,8 @@ def _same_device(cache, tensors):
 def _call(name, dev, stream, *args):
     """Entry point `name` on device `dev` and its current stream (or `stream`)."""
     fn = getattr(_lib or lib(), name)
+    if stream is not None and stream.device_index != dev:
+        raise ValueError("the stream is on cuda:%d, the cache on cuda:%d" % (stream.device_index, dev))
     s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == dev:
         st = fn(*args, s)
@@ -563,6 +566,12 @@ def _call(name, dev, stream, *args):
             st = fn(*args, s)
     if st != 0:
         raise HeadQError(name, st)
+
+
+def _zeros(shape, dtype, device, stream):
+    """Zeros made on the stream that the call runs on."""
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        return torch.zeros(shape, dtype=dtype, device=device)
 
 
 def _rows(t, name, heads, d, written=False):
@@ -653,7 +662,7 @@ def headq_cache_read(cache, U, seq_lens=None, cu=None, n=None, T=None, rows=None
                 raise ValueError("rows is needed (with cu), or n")
             rows = cache.B * n
         shape = (rows, cache.Hkv, cache.d)
-        k_out, v_out = (torch.zeros(shape, dtype=dtype, device=cache.k_codes.device) for _ in "kv")
+        k_out, v_out = (_zeros(shape, dtype, cache.k_codes.device, stream) for _ in "kv")
     have = [t.shape[0] for t in (k_out, v_out) if t is not None]
     if len(set(have)) > 1 or (rows is not None and rows != have[0]):
         raise ValueError("k_out and v_out must have the same rows")
@@ -666,12 +675,13 @@ def headq_cache_read(cache, U, seq_lens=None, cu=None, n=None, T=None, rows=None
     return k_out, v_out
 
 
-def tree_workspace(cache, Hq, n, T=None):
-    """A zeroed device workspace for headq_tree_attn with up to n new tokens per sequence."""
+def tree_workspace(cache, Hq, n, T=None, stream=None):
+    """A zeroed device workspace for headq_tree_attn with up to n new tokens per sequence and
+    lengths up to T (None: the capacity)."""
     cs = cache.struct()
     with torch.cuda.device(cache.k_codes.device):
         nb = lib().headq_tree_workspace_bytes(cs, Hq, int(n), cache.T_cap if T is None else int(T))
-    return torch.zeros(max(nb, 256), dtype=torch.uint8, device=cache.k_codes.device)
+    return _zeros(max(nb, 256), torch.uint8, cache.k_codes.device, stream)
 
 
 def headq_tree_attn(cache, q, U, mask=None, seq_lens=None, cu=None, n=None, T=None, sm_scale=None,
@@ -690,7 +700,7 @@ def headq_tree_attn(cache, q, U, mask=None, seq_lens=None, cu=None, n=None, T=No
     if Hq == 0 or Hq % cache.Hkv:
         raise ValueError("Hq must be a multiple of Hkv")
     if out is None:
-        out = torch.zeros((rows, Hq, cache.d), dtype=q.dtype, device=q.device)
+        out = _zeros((rows, Hq, cache.d), q.dtype, q.device, stream)
     qs, os_ = _rows(q, "q", Hq, cache.d), _rows(out, "out", Hq, cache.d, True)
     if out.shape[0] != rows or out.dtype != q.dtype:
         raise ValueError("out must have q's rows and dtype")
@@ -708,7 +718,7 @@ def headq_tree_attn(cache, q, U, mask=None, seq_lens=None, cu=None, n=None, T=No
             raise ValueError("mask must be [%d, %d] or [%d, %d, %d]" % (sp.n, sp.n, cache.B, sp.n, sp.n))
         mp = mask.data_ptr()
     if ws is None:
-        ws = tree_workspace(cache, Hq, sp.n, sp.T)
+        ws = tree_workspace(cache, Hq, sp.n, sp.T, stream)
     sm = 1.0 / math.sqrt(cache.d) if sm_scale is None else float(sm_scale)
     _call("headq_tree_attn", dev, stream, cache.struct(), qs, Hq, mp, ms, sp, _basis(cache, U), sm,
           int(corr_sign), os_, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel())

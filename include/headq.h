@@ -464,11 +464,13 @@ headq_status headq_cache_read(const headq_cache *cache, const headq_span *span, 
  *   mask  uint8 [n, n] of sequence b at mask + b * mask_stride bytes, row i column j
  *         nonzero when new token i sees new token j (mask_stride 0: one tree for all).
  *         NULL: j <= i, a plain run of new tokens (mask_stride is then ignored).
- *   ws    headq_tree_workspace_bytes(...) bytes, zero-filled before first use; its first
- *         word is the device error word.  Calls sharing it must not overlap on the GPU.
+ *   ws    headq_tree_workspace_bytes(cache, Hq, n, T) bytes, which serve every call of up to
+ *         n new tokens a sequence and span->T up to T; zero-filled before first use; its
+ *         first word is the device error word.  Calls sharing it must not overlap on the GPU.
  * bf16 q with bf16 or 2-bit values, d 64 or 128 and r 0, 8 or 16 runs on the tensor cores:
  * keys are rounded to 11 bits relative to the largest of their tile and softmax weights
- * to bf16, so out carries about 2 roundings to bf16.  Every other shape, and fp32 q, is
+ * to bf16, so out carries about 2 roundings to bf16.  Of those, calls with n = 1 and
+ * Hq / Hkv <= 8 run the kernels of headq_decode_attn.  Every other shape, and fp32 q, is
  * computed in fp32.  HEADQ_K_TOKEN caches only.
  */
 headq_status headq_tree_attn(const headq_cache *cache, const headq_rows *q, int Hq,

@@ -1,0 +1,198 @@
+"""headq_tree_attn of single tokens, and one workspace under calls of many sizes."""
+
+import numpy as np
+import pytest
+import torch
+
+from packed_helpers import Cache, check_tree, ref_tree, spans, tree_masks
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def hq():
+    from bit_decode_attention_sm_b200 import headq
+    return headq
+
+
+SINGLES = [  # B, Hq, Hkv, T_cap, d, r, vmode, page, lens
+    (4, 28, 4, 1024, 128, 16, "dense", 0, [1024, 1, 65, 700]),
+    (3, 8, 1, 2048, 128, 16, "2bit", 256, [2000, 64, 1]),
+    (3, 32, 8, 512, 64, 8, "dense", 64, [512, 63, 130]),
+    (2, 4, 4, 512, 128, 0, "dense", 0, [511, 2]),
+    (2, 6, 2, 256, 64, 16, "2bit", 0, [256, 17]),
+    (2, 5, 1, 256, 128, 8, "2bit", 64, [200, 256]),
+    (2, 16, 1, 512, 128, 16, "dense", 0, [512, 129]),      # more query heads than the decode takes
+    (2, 4, 2, 256, 128, 0, "2bit", 0, [255, 3]),           # a shape only the tree kernel takes
+]
+
+
+def single_case(i, seed=0):
+    B, Hq, Hkv, T_cap, d, r, vmode, page, lens = SINGLES[i]
+    rng = np.random.default_rng(1000 * seed + i)
+    c = Cache(i + 70 * seed, B, Hkv, T_cap, d, r, vmode, BF, page)
+    q = torch.from_numpy(rng.standard_normal((B, Hq, d)).astype(np.float32) * 1.5).cuda().to(BF)
+    return c, q, lens
+
+
+@pytest.mark.parametrize("sigma", [1, 0, -1])
+@pytest.mark.parametrize("i", range(len(SINGLES)))
+def test_single(i, sigma):
+    c, q, lens = single_case(i)
+    lse = torch.full(q.shape[:2], 9.0, device="cuda")
+    ws = hq().tree_workspace(c.hq, q.shape[1], 1)
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kw = dict(seq_lens=sl, corr_sign=sigma, ws=ws)
+    out = hq().headq_tree_attn(c.hq, q, c.U, lse=lse, **kw)
+    hq().headq_workspace_status(ws)
+    check_tree(out, lse, ref_tree(c, q, [1] * len(lens), lens, None, sigma=float(sigma)))
+    assert torch.equal(out, hq().headq_tree_attn(c.hq, q, c.U, **kw))
+
+
+@pytest.mark.parametrize("i", range(len(SINGLES)))
+def test_some_sequences_have_a_token_and_some_see_themselves(i):
+    c, q, lens = single_case(i, 1)
+    B = len(lens)
+    counts = [b % 2 for b in range(B)][::-1]                # the last sequence has one
+    cu, sl = spans(counts, lens)
+    for see in (False, True):
+        mask = np.full((1, 1), see)
+        big = torch.full((B, q.shape[1], q.shape[2] + 8), 7.0, dtype=BF, device="cuda")
+        lse = torch.full((B, q.shape[1]), 7.0, device="cuda")
+        hq().headq_tree_attn(c.hq, q, c.U, mask=torch.from_numpy(mask).cuda(), seq_lens=sl, cu=cu, n=1,
+                             out=big[:, :, 8:], lse=lse)
+        rows = sum(counts)
+        ref = ref_tree(c, q[:rows], counts, lens, np.broadcast_to(mask, (B, 1, 1)))
+        check_tree(big[:rows, :, 8:], lse[:rows], ref)
+        assert (big[rows:] == 7).all() and (big[:, :, :8] == 7).all() and (lse[rows:] == 7).all()
+
+
+@pytest.mark.parametrize("i", [0, 1, 2, 4])
+def test_single_rows_that_see_nothing(i):
+    """No cached token at all, a sequence of its own unseen token, one with more new tokens
+    than n, and one with more than it has cached."""
+    c, q, _ = single_case(i, 2)
+    B, Hq, d = q.shape
+    lens = [0, 1, 5, 3][:B]
+    counts = [1, 1, 3, 4][:B]
+    cu, sl = spans(counts, lens)
+    rows = sum(counts)
+    qq = torch.randn(rows, Hq, d, device="cuda").to(BF)
+    out, lse = torch.full_like(qq, 7.0), torch.full((rows, Hq), 7.0, device="cuda")
+    mask = torch.zeros(1, 1, dtype=torch.bool, device="cuda")
+    hq().headq_tree_attn(c.hq, qq, c.U, mask=mask, seq_lens=sl, cu=cu, n=1, out=out, lse=lse)
+    assert (out[:2] == 0).all() and (lse[:2] == -np.inf).all()
+    if B > 2:                                              # its first row sees the two before it
+        first = ref_tree(c, qq[2:3].repeat(B, 1, 1), [1] * B, [0, 0, 2, 0][:B], np.ones((B, 1, 1), bool))
+        check_tree(out[2:3], lse[2:3], [a[2:3] for a in first])
+        assert (out[3:5] == 7).all() and (lse[3:5] == 7).all()
+    if B > 3:
+        assert (out[5] == 0).all() and (lse[5] == -np.inf).all() and (out[6:] == 7).all()
+
+
+@pytest.mark.parametrize("poison", ["nan", "inf", "huge"])
+@pytest.mark.parametrize("i", range(len(SINGLES)))
+def test_what_lies_behind_a_sequence_is_not_felt(i, poison):
+    c, q, lens = single_case(i, 3)
+    clean = ref_tree(c, q, [1] * len(lens), lens, None)
+    x = {"nan": float("nan"), "inf": float("inf"), "huge": 3e38}[poison]
+    for b, T in enumerate(lens):
+        for t in range(T, c.hq.T_cap):
+            slab, off = (b, t) if c.table is None else (int(c.table[b, t // c.hq.page_size]), t % c.hq.page_size)
+            for name in ("k_scale", "k_min", "z_scale", "v", "v_scale", "v_min"):
+                if name in c.planes:
+                    c.planes[name][slab, :, off] = x
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    check_tree(hq().headq_tree_attn(c.hq, q, c.U, seq_lens=sl), None, clean)
+
+
+@pytest.mark.parametrize("mag", [(1e-3, 1.0), (300.0, 1e-2), (1e4, 1e-4), (1.0, 1e3)])
+@pytest.mark.parametrize("i", [0, 1])
+def test_single_magnitudes(i, mag):
+    c, q, lens = single_case(i, 4)
+    q = (q.float() * mag[0]).to(BF)
+    for n in ("k_scale", "k_min", "z_scale"):
+        c.planes[n] *= mag[1]
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    out = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=sl, lse=lse)
+    check_tree(out, lse, ref_tree(c, q, [1] * len(lens), lens, None))
+
+
+@pytest.mark.parametrize("qd", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (28, 4), (16, 1)])
+def test_one_workspace_for_smaller_calls(Hq, Hkv, qd):
+    """A workspace serves every call of fewer new tokens and shorter sequences, in any order,
+    whatever an earlier call of another shape left in it."""
+    c = Cache(31, 2, Hkv, 4096, 128, 16)
+    L = hq().lib()
+    ws = hq().tree_workspace(c.hq, Hq, 260)
+    rng = np.random.default_rng(5)
+    for n, T in [(260, 4096), (1, 4096), (129, 4096), (128, 900), (1, 64), (37, 3000), (1, 4096), (2, 129)]:
+        assert L.headq_tree_workspace_bytes(c.hq.struct(), Hq, n, T) <= ws.numel()
+        q = torch.from_numpy(rng.standard_normal((2 * n, Hq, 128)).astype(np.float32)).cuda().to(qd)
+        lens = [T, max(n, T // 3)]
+        mask = tree_masks(rng, 2, min(n, 8))
+        if n > 8:
+            mask = np.broadcast_to(np.tril(np.ones((n, n), bool)), (2, n, n)).copy()
+            mask[:, ::3, :n // 2] = False
+        sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        out = hq().headq_tree_attn(c.hq, q, c.U, mask=torch.from_numpy(mask).cuda(), seq_lens=sl, n=n, T=T, ws=ws)
+        fresh = hq().headq_tree_attn(c.hq, q, c.U, mask=torch.from_numpy(mask).cuda(), seq_lens=sl, n=n, T=T)
+        assert torch.equal(out, fresh)
+        if n <= 37:
+            check_tree(out, None, ref_tree(c, q, [n, n], lens, mask))
+    hq().headq_workspace_status(ws)
+
+
+def test_workspace_bounds():
+    """The bytes grow with n and T, so that a workspace holds every smaller call's."""
+    L = hq().lib()
+    for B, Hq, Hkv in [(1, 8, 8), (3, 28, 4), (16, 40, 40), (200, 8, 1), (1, 16, 1)]:
+        c = Cache(1, B, Hkv, 64, 128, 16)
+        s = c.hq.struct()
+        size = [[L.headq_tree_workspace_bytes(s, Hq, n, T) for T in (1, 100, 1000, 4096, 9999, 50000, 131072)]
+                for n in (1, 2, 16, 18, 19, 64, 127, 128, 129, 500)]
+        size = np.array(size, dtype=np.float64)
+        assert (size > 0).all() and (np.diff(size, axis=0) >= 0).all() and (np.diff(size, axis=1) >= 0).all()
+
+
+def test_single_captured_and_replayed():
+    c, q, lens = single_case(0, 6)
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws, ws2 = (hq().tree_workspace(c.hq, q.shape[1], 1) for _ in range(2))
+    out = torch.zeros_like(q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        hq().headq_tree_attn(c.hq, q, c.U, seq_lens=sl, out=out, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        hq().headq_tree_attn(c.hq, q, c.U, seq_lens=sl, out=out, ws=ws)
+    for step in range(3):
+        q.copy_(torch.randn(q.shape, device="cuda"))
+        sl.copy_(torch.tensor([n - (step if n > 9 else 0) for n in lens], dtype=torch.int32))
+        torch.cuda.synchronize()
+        g.replay()
+        eager = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=sl, ws=ws2, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
+        check_tree(out, None, ref_tree(c, q, [1] * len(lens), sl.tolist(), None))
+
+
+def test_allocations_follow_the_stream():
+    """Outputs and workspaces that a call makes are made on the stream it runs on."""
+    c, q, lens = single_case(0, 7)
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=sl)
+    k0, v0 = hq().headq_cache_read(c.hq, c.U, seq_lens=sl, n=1)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    x = torch.randn(4096, 4096, device="cuda")
+    for _ in range(5):                                     # work that the current stream is busy with
+        x = (x @ x).clamp_(-1, 1)
+    got = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=sl, stream=side)
+    k1, v1 = hq().headq_cache_read(c.hq, c.U, seq_lens=sl, n=1, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(k0, k1) and torch.equal(v0, v1)
