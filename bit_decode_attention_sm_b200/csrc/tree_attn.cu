@@ -31,6 +31,14 @@ constexpr float kLog2e = 1.4426950408889634f;
 // same chunk fall in distinct banks
 __host__ __device__ inline int row_chunks(int d, int r) { return ((d + r + 3) / 4) | 1; }
 
+// four elements of a tensor that is fp32 or bf16, from a multiple of 4
+__device__ __forceinline__ float4 load4(const void* base, long long off, bool bf16) {
+  if (!bf16) return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
+  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + off);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 tree_any_kernel(const TreeParams p) {
@@ -55,14 +63,15 @@ tree_any_kernel(const TreeParams p) {
   // query rows, then U_h^T q
   const bool qb = p.q.dtype == HEADQ_BF16;
   float* qf = reinterpret_cast<float*>(q_s);
-  for (int e = tid; e < kRT * D; e += kThreads) {
-    const int x = e / D, c = e - x * D, xr = x0 + x;
-    float v = 0.0f;
+#pragma unroll 4
+  for (int e = tid; e < kRT * (D / 4); e += kThreads) {
+    const int x = e / (D / 4), c4 = e - x * (D / 4), xr = x0 + x;
+    float4 v = make_float4(0, 0, 0, 0);
     if (xr < rows) {
       const int i = xr / p.G, g = xr - i * p.G;
-      v = load_elem(p.q.ptr, (sq.row0 + i) * p.q.row_stride + (kv * p.G + g) * p.q.head_stride + c, qb);
+      v = load4(p.q.ptr, (sq.row0 + i) * p.q.row_stride + (kv * p.G + g) * p.q.head_stride + 4 * c4, qb);
     }
-    qf[x * rc * 4 + c] = v;
+    q_s[x * rc + c4] = v;
   }
   __syncthreads();
   const int r4 = (r + 3) / 4 * 4;
@@ -71,6 +80,7 @@ tree_any_kernel(const TreeParams p) {
     float a = 0.0f;
     if (i < r) {
       const float* up = p.U + static_cast<size_t>(kv) * D * r + i;
+#pragma unroll 16
       for (int c = 0; c < D; ++c) a = fmaf(qf[x * rc * 4 + c], up[c * r], a);
     }
     qf[x * rc * 4 + D + i] = a * p.corr_sign;
@@ -83,6 +93,7 @@ tree_any_kernel(const TreeParams p) {
 #pragma unroll
   for (int k = 0; k < NC; ++k) acc[k] = make_float4(0, 0, 0, 0);
   const int sy = tid >> 4, sx = tid & 15;  // logits of rows sy, sy+16 x tokens sx, sx+16
+  const int node[2] = {(x0 + sy) / p.G, (x0 + sy + 16) / p.G};
   const int len4 = (D + r4) / 4;
 
   for (int t0 = t_lo; t0 < t_hi; t0 += kTT) {
@@ -101,12 +112,8 @@ tree_any_kernel(const TreeParams p) {
         k = decode4(p.c.k_codes[row * (D / 4) + c4], p.c.k_scale[gr], p.c.k_min[gr]);
         if (p.c.vmode == HEADQ_V_2BIT) {
           v = decode4(p.c.v_codes[row * (D / 4) + c4], p.c.v_scale[gr], p.c.v_min[gr]);
-        } else if (p.c.v_dtype == HEADQ_F32) {
-          v = reinterpret_cast<const float4*>(p.c.v)[row * (D / 4) + c4];
         } else {
-          const uint2 u = reinterpret_cast<const uint2*>(p.c.v)[row * (D / 4) + c4];
-          v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                          __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+          v = load4(p.c.v, row * D + 4 * c4, p.c.v_dtype == HEADQ_BF16);
         }
       }
       k_s[tt * rc + c4] = k;
@@ -143,7 +150,7 @@ tree_any_kernel(const TreeParams p) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int x = x0 + sy + 16 * i, t = t0 + sx + 16 * j;
-        const bool see = x < rows && t < t_hi && (t < sq.p0 || tree_sees(p, b, x / p.G, t - sq.p0));
+        const bool see = x < rows && t < t_hi && (t < sq.p0 || tree_sees(p, b, node[i], t - sq.p0));
         s_s[(sy + 16 * i) * (kTT + 1) + sx + 16 * j] = see ? s[i][j] * p.sm_scale : -INFINITY;
       }
     __syncthreads();
@@ -235,7 +242,7 @@ tree_merge_kernel(const TreeParams p) {
   float4 acc[NC];
 #pragma unroll
   for (int k = 0; k < NC; ++k) acc[k] = make_float4(0, 0, 0, 0);
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < p.splits; ++s) {
     const float4 ml = p.part_ml[pr + s * ru];
     const float w = exp2f((ml.x - base) * kLog2e);
