@@ -15,6 +15,7 @@ headq_status check_span(const headq_span* s, const headq_cache* c) {
   if (s->seq_lens && !aligned16(s->seq_lens)) return HEADQ_ERR_INVALID_ARG;
   if (s->cu && !aligned16(s->cu)) return HEADQ_ERR_INVALID_ARG;
   if (!s->cu && static_cast<long long>(c->B) * s->n > s->rows) return HEADQ_ERR_INVALID_ARG;
+  if (s->T > 1 << 30 || s->rows > 1 << 30) return HEADQ_ERR_UNSUPPORTED;  // the kernels' indices are int
   return c->B > 65535 || c->Hkv > 65535 ? HEADQ_ERR_UNSUPPORTED : HEADQ_OK;
 }
 
@@ -103,6 +104,7 @@ HEADQ_API headq_status headq_cache_write_ragged(const headq_cache* cache, const 
   p.in_bf16 = k->dtype == HEADQ_BF16;
   p.U = U;
   p.span = *span;
+  p.span.n = std::min(span->n, span->rows);  // a sequence has no more rows than there are
   p.src = src;
   p.src_rows = src_rows;
   return launch_cache_write_ragged(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -125,6 +127,7 @@ HEADQ_API headq_status headq_cache_read(const headq_cache* cache, const headq_sp
   CacheReadParams p{};
   p.c = *cache;
   p.span = *span;
+  p.span.n = std::min(span->n, span->rows);
   p.U = U;
   p.sigma = static_cast<float>(corr_sign);
   if (k_out) p.k = *k_out;

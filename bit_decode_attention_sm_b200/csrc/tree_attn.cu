@@ -293,21 +293,25 @@ tree_one_prep_kernel(const TreeParams p, const TreeOne w) {
   }
 }
 
-// their results to the packed rows
+// Their results to the packed rows.  The decode kernels give 0 and -inf for a sum of weights
+// that is not positive, not-a-number included; here only a row that sees nothing has that.
 __global__ void __launch_bounds__(256)
 tree_one_finish_kernel(const TreeParams p, const TreeOne w) {
   const int b = blockIdx.x, tid = threadIdx.x;
   const SpanSeq sq = span_seq(p.span, b);
   if (sq.n == 0) return;
   const int per = p.c.d / 4;
+  const size_t r0 = static_cast<size_t>(b) * p.Hq;
+  const bool sees = w.lens[b] > 0;
   for (int e = tid; e < p.Hq * per; e += 256) {
     const int h = e / per, c4 = e - h * per;
-    store_row4(p.out, sq.row0 * p.out.row_stride + h * p.out.head_stride + 4 * c4,
-               reinterpret_cast<const float4*>(w.out)[static_cast<size_t>(b) * p.Hq * per + e]);
+    float4 o = reinterpret_cast<const float4*>(w.out)[r0 * per + e];
+    const float lse = w.lse[r0 + h];
+    const bool nan = sees && lse == -INFINITY;
+    if (nan) o.x = o.y = o.z = o.w = NAN;
+    store_row4(p.out, sq.row0 * p.out.row_stride + h * p.out.head_stride + 4 * c4, o);
+    if (p.lse && c4 == 0) p.lse[static_cast<size_t>(sq.row0) * p.Hq + h] = nan ? NAN : lse;
   }
-  if (p.lse)
-    for (int h = tid; h < p.Hq; h += 256)
-      p.lse[static_cast<size_t>(sq.row0) * p.Hq + h] = w.lse[static_cast<size_t>(b) * p.Hq + h];
 }
 
 template <int D>

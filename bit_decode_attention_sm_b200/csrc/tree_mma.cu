@@ -761,7 +761,8 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
 #pragma unroll
       for (int g = 0; g < HG; ++g) {
         const float m = (half ? cur.km[HG + g] : cur.km[g]) * sc.x, d = (half ? cur.ks[HG + g] : cur.ks[g]) * sc.x;
-        const uint32_t l01 = pack_f16(m, m + d), l23 = pack_f16(fmaf(2.0f, d, m), fmaf(3.0f, d, m));
+        // code 0 with its product too: a scale that is not finite makes all four levels NaN or infinite
+        const uint32_t l01 = pack_f16(fmaf(0.0f, d, m), m + d), l23 = pack_f16(fmaf(2.0f, d, m), fmaf(3.0f, d, m));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint4 a, c;
@@ -791,7 +792,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
 #pragma unroll
         for (int g = 0; g < HG; ++g) {
           const float m = cur.vm[g], d = cur.vs[g];
-          uint32_t l01 = pack_bf16(m, m + d), l23 = pack_bf16(fmaf(2.0f, d, m), fmaf(3.0f, d, m));
+          uint32_t l01 = pack_bf16(fmaf(0.0f, d, m), m + d), l23 = pack_bf16(fmaf(2.0f, d, m), fmaf(3.0f, d, m));
           // a new token's value that is not finite must not meet the zero weights of the
           // rows that do not see it: it is left out here and added to the rows that do
           if (t0 + tok >= t_hi) l01 = l23 = 0u;

@@ -196,3 +196,76 @@ def test_allocations_follow_the_stream():
     k1, v1 = hq().headq_cache_read(c.hq, c.U, seq_lens=sl, n=1, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(k0, k1) and torch.equal(v0, v1)
+
+
+@pytest.mark.parametrize("name", ["k_scale", "k_min", "v", "v_scale"])
+@pytest.mark.parametrize("i", range(len(SINGLES)))
+def test_a_seen_token_that_is_not_a_number_is_felt(i, name):
+    c, q, lens = single_case(i, 8)
+    if name not in c.planes:
+        return
+    clean = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    t = lens[0] // 2                                       # one token of the first sequence
+    slab, off = (0, t) if c.table is None else (int(c.table[0, t // c.hq.page_size]), t % c.hq.page_size)
+    c.planes[name][slab, :, off] = float("nan")
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=sl)
+    assert out[0].isnan().all() and torch.equal(out[1:], clean[1:])
+
+
+@pytest.mark.parametrize("n,qd,Hq", [(1, BF, 8), (1, BF, 32), (6, BF, 8), (70, BF, 8), (6, F32, 8)])
+def test_a_query_that_is_not_a_number_spoils_its_own_row(n, qd, Hq):
+    c = Cache(41, 2, 2, 512, 128, 16)
+    rng = np.random.default_rng(n)
+    q = torch.from_numpy(rng.standard_normal((2 * n, Hq, 128)).astype(np.float32)).cuda().to(qd)
+    sl = torch.tensor([500, 201], dtype=torch.int32, device="cuda")
+    clean = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=sl, n=n)
+    q[n, 3, 5] = float("nan")
+    q[0, 1, 9] = float("inf")
+    out = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=sl, n=n)
+    assert out[n, 3].isnan().all() and not torch.isfinite(out[0, 1]).any()
+    out[n, 3] = clean[n, 3]
+    out[0, 1] = clean[0, 1]
+    assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("vmode,B", [("dense", 33), ("2bit", 65)])
+def test_offsets_past_32_bits(vmode, B):
+    """The last sequence of a cache whose planes pass 2^32 elements (dense values) and 2^31
+    bytes (codes): written, read and attended to as in a cache of its own."""
+    Hkv, T, d, r = 8, 131072, 128, 16
+    rows = B * Hkv * T
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    assert rows * (d if vmode == "dense" else d // 4) > (1 << 32 if vmode == "dense" else 1 << 31)
+    kw = dict(vmode=vmode)
+    big = hq().HeadQCache(B, Hkv, T, d, r, **kw)
+    one = Cache(51, 1, Hkv, 512, d, r, vmode)
+    rng = np.random.default_rng(7)
+    kv = torch.from_numpy(rng.standard_normal((40, 2 * Hkv, d)).astype(np.float32)).cuda().to(BF)
+    for name, t in one.planes.items():
+        getattr(big, name).view(B, Hkv, T, -1)[B - 1, :, T - 512:] = t.view(1, Hkv, 512, -1)[0]
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[B] = 40
+    hq().headq_cache_write_ragged(one.hq, kv[:, :Hkv], kv[:, Hkv:], one.U)
+    hq().headq_cache_write_ragged(big, kv[:, :Hkv], kv[:, Hkv:], one.U, cu=cu, n=40)
+    for name, t in one.planes.items():
+        assert torch.equal(getattr(big, name).view(B, Hkv, T, -1)[B - 1, :, T - 512:], t.view(1, Hkv, 512, -1)[0]), name
+    cu[B] = 512
+    for x, y in zip(hq().headq_cache_read(big, one.U, cu=cu, n=512, rows=512),
+                    hq().headq_cache_read(one.hq, one.U, n=512)):
+        assert torch.equal(x, y)
+    # attention: the other tokens' keys are minus infinity's stand-in, so only the last 512 count
+    big.k_min[B - 1, :, :T - 512] = 0.0
+    big.k_scale[B - 1, :, :T - 512] = 0.0
+    big.z_scale[B - 1, :, :T - 512] = 0.0
+    for n, q_dtype in [(1, BF), (40, BF), (5, F32)]:
+        U0 = torch.zeros_like(one.U)                       # no correction: a logit is q . k^base
+        q = torch.full((n, Hkv, d), 0.0, device="cuda", dtype=q_dtype)
+        q[..., 0] = 1.0
+        base = hq().headq_cache_read(one.hq, U0, n=512, dtype=F32)[0][..., 0]
+        one.planes["k_min"][..., 0] += 200.0 - base.min()  # channel 0 of the last 512 is at least 200
+        big.k_min.view(B, Hkv, T, -1)[B - 1, :, T - 512:] = one.planes["k_min"][0]
+        cu[B] = n
+        got = hq().headq_tree_attn(big, q, U0, cu=cu, n=n, sm_scale=1.0)
+        check_tree(got, None, ref_tree(one, q, [n], [512], None, sm=1.0, sigma=0.0))

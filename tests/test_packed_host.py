@@ -104,3 +104,14 @@ def test_binding_refuses_what_is_not_on_a_gpu(hq):
     with pytest.raises(ValueError):
         hq.HeadQCache.from_planes(torch.zeros(1, 2, 16, 32, dtype=torch.uint8), torch.zeros(1, 2, 16, 4),
                                   torch.zeros(1, 2, 16, 4))   # no values
+
+
+def test_sizes_past_the_kernels_indices(hq):
+    """More than 2^30 packed rows, or lengths, are refused; n may be any bound of n_b."""
+    big = make_cache(hq, T_cap=(1 << 30) + 64)
+    for sp, want in [(span(hq, n=1, rows=(1 << 30) + 1), 2), (span(hq, n=4, T=(1 << 30) + 16), 2)]:
+        assert write(hq, big, src=FAKE, sp=sp) == want
+        assert read(hq, big, sp=sp) == want
+    far = (1 << 31) - 1
+    assert write(hq, sp=span(hq, n=far, rows=0, cu=FAKE), src_rows=0) == 0
+    assert read(hq, sp=span(hq, n=far, rows=0, cu=FAKE)) == 0
