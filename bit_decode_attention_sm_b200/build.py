@@ -7,8 +7,8 @@ into ``bit_decode_attention_sm_b200/libheadq.so``.  The shared codec
 (``codec.cuh``) states every step with explicit round-to-nearest intrinsics
 (``__fmul_rn``, ``__fadd_rn``, ``mul.rn.f32x2``/``add.rn.f32x2``), which the
 compiler never contracts, so it is bit-exact in every file that includes it;
-``cache_write.cu`` is also compiled with ``-fmad=false`` for its own arithmetic
-around the codec.  No file uses fast-math, so division, square root and
+``cache_write.cu`` and ``cache_write_ragged.cu`` are also compiled with
+``-fmad=false`` for their own arithmetic around the codec.  No file uses fast-math, so division, square root and
 denormals keep IEEE semantics.
 """
 
