@@ -43,6 +43,28 @@ size_t tree_mma_image_bytes(const headq_cache& c);
 cudaError_t launch_tree_mma(const TreeParams& p, const TreeMma& t, int grid_splits, bool pair, cudaStream_t s);
 cudaError_t launch_tree(const TreeParams& p, const TreeMma& t, const TreePlan& plan, cudaStream_t s);
 
+// Programmatic dependent launch: the kernel may start while the one before it in the stream is
+// ending (from that one's launch_dependents on); whatever reads its results, and every CTA
+// before it ends, first waits for it to be complete.
+__device__ __forceinline__ void wait_for_prior_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                         const Args&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // whether new token i of sequence b sees its new token j (both below span.n)
 __device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int i, int j) {
   return p.mask ? p.mask[b * p.mask_stride + static_cast<long long>(i) * p.span.n + j] != 0 : j <= i;

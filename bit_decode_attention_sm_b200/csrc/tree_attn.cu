@@ -227,6 +227,7 @@ tree_any_kernel(const TreeParams p) {
 template <int D>
 __global__ void __launch_bounds__(128)
 tree_merge_kernel(const TreeParams p) {
+  wait_for_prior_kernel();
   const int unit = blockIdx.y, b = unit / p.c.Hkv, kv = unit - b * p.c.Hkv;
   const SpanSeq sq = span_seq(p.span, b);
   const int x = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -332,8 +333,7 @@ cudaError_t launch_any(const TreeParams& p, cudaStream_t s) {
 template <int D>
 cudaError_t launch_merge(const TreeParams& p, cudaStream_t s) {
   dim3 grid((p.span.n * p.G + 3) / 4, p.c.B * p.c.Hkv);
-  tree_merge_kernel<D><<<grid, 128, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(tree_merge_kernel<D>, grid, 128, 0, s, p);
 }
 
 }  // namespace

@@ -184,6 +184,7 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Shared-memory matrix descriptors: low word, start address and leading byte offset; high
@@ -270,6 +271,7 @@ constexpr int kPrepRows = 8;
 template <int D, int R>
 __global__ void __launch_bounds__(256)
 tree_prep_kernel(const TreeParams p, const TreeMma t, int row_ctas) {
+  let_next_kernel_start();
   const int warp = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (static_cast<int>(blockIdx.x) >= row_ctas) {  // mask bits: one warp per (sequence, row)
     const int bi = (blockIdx.x - row_ctas) * 8 + (threadIdx.x >> 5);
@@ -571,7 +573,10 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   const int unit = blockIdx.z, b = unit / p.c.Hkv, kv = unit - b * p.c.Hkv;
   const SpanSeq sq = span_seq(p.span, b);
   const int rows = sq.n * p.G, xb = blockIdx.x * (PAIR ? 2 : 1) * kBlock;
-  if (xb >= rows) return;
+  if (xb >= rows) {
+    wait_for_prior_kernel();
+    return;
+  }
   const int P = sq.p0, L = sq.p0 < 0 ? 0 : sq.p0 + sq.n;
   const int t_lo = blockIdx.y * p.chunk, t_hi = min(L, t_lo + p.chunk);
   const int tiles = t_hi > t_lo ? (t_hi - t_lo + kTile - 1) / kTile : 0;
@@ -582,6 +587,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
   const int x = xb + (PAIR ? wl * kBlock : 0) + (warp & 3) * 32 + lane;
 
   if (tiles == 0) {  // nothing to read: the rows' share of this split is empty
+    wait_for_prior_kernel();
     if (warp < 8 && x < rows && (PAIR || wl < lane_parts)) {
       if (p.splits > 1) {
         p.part_ml[(static_cast<size_t>(unit) * p.splits + blockIdx.y * lane_parts + (PAIR ? 0 : wl)) * part_rows + x] =
@@ -654,6 +660,8 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kTmaWarp) {
     if (lane == 0) {
+      wait_for_prior_kernel();  // the query images; the decoders are at work on the cache meanwhile
+      fence_async_global();
       const int nq = PAIR ? lanes_on : 1;
       mbar_expect_tx(q_full, nq * Ly::kOperand);
       const uint8_t* img = t.qimg + (static_cast<size_t>(unit) * t.blocks + xb / kBlock) * Ly::kOperand;
@@ -845,6 +853,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     // ---- softmax and epilogue of this warp's 32 query rows
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + 128 * wl + lane_off, to = tmem + 256 + 128 * wl + lane_off;
+    wait_for_prior_kernel();
     const int i = min(x, rows - 1) / p.G;
     const float fq = t.qf[static_cast<size_t>(unit) * t.blocks * kBlock + x];
     const uint32_t* words = t.words ? t.words + (static_cast<size_t>(b) * p.span.n + i) * t.wpr : nullptr;
@@ -914,6 +923,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       if (!handed) hand_over();
     }
     const float m = st.m, l = st.l, lx = st.lx;
+    let_next_kernel_start();
     if (ok && nk > 0 && !mbar_wait(o_done(wl, 1), (nk - 1) & 1)) ok = false;
     tc_fence_after();
     if (ok) {
@@ -994,8 +1004,7 @@ cudaError_t launch_main(const TreeParams& p, const TreeMma& t, int grid_splits, 
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   dim3 grid((t.blocks + (PAIR ? 1 : 0)) / (PAIR ? 2 : 1), grid_splits, p.c.B * p.c.Hkv);
-  k<<<grid, kThreads, smem, s>>>(p, t, map);
-  return cudaGetLastError();
+  return launch_after(k, grid, kThreads, smem, s, p, t, map);
 }
 
 template <int D, int R>
