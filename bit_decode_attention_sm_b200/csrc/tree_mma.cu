@@ -264,9 +264,11 @@ __device__ __forceinline__ void pick16(uint32_t w, uint32_t l01, uint32_t l23, u
 }
 
 // ---------------------------------------------------------------- prep
-// One warp per 8 query rows of a unit's row blocks: D / 4 lanes a row, 4 operand positions
-// each.  Blocks past the rows' part pack the mask.
-constexpr int kPrepRows = 8;
+// One warp per 4 query rows of a unit's row blocks: D / 4 lanes a row, 4 operand positions
+// each; all rows are loaded before the first is worked on, since the main kernel waits for the
+// last (one row at a time, 8 rows to a warp, took it 5 us longer).  Blocks past the rows' part
+// pack the mask.
+constexpr int kPrepRows = 4;
 
 template <int D, int R>
 __global__ void __launch_bounds__(256)
@@ -309,16 +311,27 @@ tree_prep_kernel(const TreeParams p, const TreeMma t, int row_ctas) {
       }
   }
   const float sign = p.sm_scale < 0.0f ? -1.0f : 1.0f;
-  for (int it = 0; it < kPrepRows / RPW; ++it) {
+  constexpr int IT = kPrepRows / RPW;
+  uint16_t qr[IT][4];
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
     const int x = x0 + it * RPW + lane / LPR;
-    float q[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) qr[it][k] = 0;
     if (x < rows) {
       const int i = x / p.G, g = x - i * p.G;
       const uint16_t* src = static_cast<const uint16_t*>(p.q.ptr) + (sq.row0 + i) * p.q.row_stride +
                             (kv * p.G + g) * p.q.head_stride;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) q[k] = sign * bf16_bits_to_f32(src[ch[k]]);
+      for (int k = 0; k < 4; ++k) qr[it][k] = __ldg(src + ch[k]);
     }
+  }
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int x = x0 + it * RPW + lane / LPR;
+    float q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) q[k] = sign * bf16_bits_to_f32(qr[it][k]);
     float mx = fmaxf(fmaxf(fabsf(q[0]), fabsf(q[1])), fmaxf(fabsf(q[2]), fabsf(q[3])));
     float side = 0.0f;
     if constexpr (R > 0) {
@@ -409,6 +422,8 @@ __device__ __forceinline__ void load_f32(const float* p, float (&x)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = __uint_as_float(u[i]);
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // half `h` of the token in plane row `row`
 template <int D, int R, bool V2>
@@ -644,6 +659,23 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
+  }
+  // the first tile's planes on their way to L2 while barriers and TMEM are set up
+  if (warp >= kDecodeWarp && warp < kDecodeWarp + 4) {
+    TokenRows first(p.c, b, kv, t_lo + tid - kDecodeWarp * 32, t_hi, nullptr);
+    const long long row = first.next();
+    prefetch_l2(p.c.k_codes + row * (D / 4));
+    prefetch_l2(p.c.k_scale + row * NG);
+    prefetch_l2(p.c.k_min + row * NG);
+    if constexpr (R > 0) {
+      prefetch_l2(p.c.z_codes + row * (R / 2));
+      prefetch_l2(p.c.z_scale + row);
+    }
+    if constexpr (V2) {
+      prefetch_l2(p.c.v_codes + row * (D / 4));
+      prefetch_l2(p.c.v_scale + row * NG);
+      prefetch_l2(p.c.v_min + row * NG);
+    }
   }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(misc)) : "memory");
@@ -961,10 +993,19 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         }
         if (x < rows) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 v = make_float4(o[j] * inv, o[j + 1] * inv, o[j + 2] * inv, o[j + 3] * inv);
-            if (direct) store_row4(p.out, orow * p.out.row_stride + h * p.out.head_stride + 32 * c + j, v);
-            else *reinterpret_cast<float4*>(p.part_o + pr * D + 32 * c + j) = v;
+          for (int j = 0; j < 32; j += 8) {
+            float4 v[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              v[k] = make_float4(o[j + 4 * k] * inv, o[j + 4 * k + 1] * inv, o[j + 4 * k + 2] * inv, o[j + 4 * k + 3] * inv);
+            if (direct) {  // bf16, as the queries of this kernel are
+              uint16_t* dst = static_cast<uint16_t*>(p.out.ptr) + orow * p.out.row_stride + h * p.out.head_stride;
+              *reinterpret_cast<uint4*>(dst + 32 * c + j) = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[0].z, v[0].w),
+                                                                      pack_bf16(v[1].x, v[1].y), pack_bf16(v[1].z, v[1].w));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) *reinterpret_cast<float4*>(p.part_o + pr * D + 32 * c + j + 4 * k) = v[k];
+            }
           }
         }
       }
