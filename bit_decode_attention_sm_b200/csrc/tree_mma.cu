@@ -912,7 +912,8 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
           for (int j = 1; j < kHalf - 1; j += 2) mx = max3(mx, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
           const float top = fmaxf(mx, __uint_as_float(s[kHalf - 1])) * f;
           // the accumulator rests once the half before this one is read out
-          if (y > 0 && !mbar_wait(o_done(wl, 1 - h), ((y - 1) >> 1) & 1)) ok = false;
+          // (ok stays the same in a whole warp, which works together to the end)
+          if (y > 0) ok = __all_sync(kAll, ok && mbar_wait(o_done(wl, 1 - h), ((y - 1) >> 1) & 1));
           tc_fence_after();
           st = raise_max<D>(st, top > st.m ? top + kSlack : st.m, to, y > 0);
           weights(s, f, st.m, w, sum, bits);
@@ -938,7 +939,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         if (!__all_sync(kAll, mbar_test(bar, parity))) {  // not there yet: this one's weights first
           if (!handed) hand_over();
           handed = true;
-          if (!mbar_wait(bar, parity)) ok = false;
+          ok = __all_sync(kAll, ok && mbar_wait(bar, parity));
         }
         const int tile = tile_of(wl, (y + 1) >> 1);
         const float* col = scale_s + (tile % kRing) * kTile;
@@ -956,7 +957,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     }
     const float m = st.m, l = st.l, lx = st.lx;
     let_next_kernel_start();
-    if (ok && nk > 0 && !mbar_wait(o_done(wl, 1), (nk - 1) & 1)) ok = false;
+    if (nk > 0) ok = __all_sync(kAll, ok && mbar_wait(o_done(wl, 1), (nk - 1) & 1));
     tc_fence_after();
     if (ok) {
       const bool bad = *reinterpret_cast<volatile uint32_t*>(misc + 1) != 0u;
@@ -979,6 +980,11 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         }
         tc_wait_st();
       }
+// 32 columns at a time.  PAIR: through shared memory (the lane's query image, which its
+      // products no longer read), so that 8 lanes store one row's 128 bytes where each lane
+      // storing its own row touches 32 lines an instruction (9000 cycles a CTA).
+      float4* turn = reinterpret_cast<float4*>(sm + Ly::kQ + (PAIR ? wl : 0) * Ly::kOperand) + (warp & 3) * 256;
+      const long long off = static_cast<long long>(orow) * p.out.row_stride + h * p.out.head_stride;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t w[32];
@@ -986,25 +992,33 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         tc_wait_ld();
         float o[32];  // in channel order
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[V2 ? channel_at(j) : j] = __uint_as_float(w[j]);
-        if (l == 0.0f) {
+        for (int j = 0; j < 32; ++j) o[V2 ? channel_at(j) : j] = l == 0.0f ? 0.0f : __uint_as_float(w[j]) * inv;
+        if constexpr (PAIR) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-        }
-        if (x < rows) {
+          for (int j = 0; j < 8; ++j)
+            turn[lane * 8 + (j ^ (lane & 7))] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int row = 4 * j + (lane >> 3);
+            const float4 v = turn[row * 8 + ((lane & 7) ^ (row & 7))];
+            const long long ro = __shfl_sync(kAll, off, row);
+            if (x - lane + row >= rows) continue;
+            if (direct) store_row4(p.out, ro + 32 * c + 4 * (lane & 7), v);
+            else *reinterpret_cast<float4*>(p.part_o + (pr - lane + row) * D + 32 * c + 4 * (lane & 7)) = v;
+          }
+          __syncwarp();
+        } else if (x < rows) {
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
-            float4 v[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              v[k] = make_float4(o[j + 4 * k] * inv, o[j + 4 * k + 1] * inv, o[j + 4 * k + 2] * inv, o[j + 4 * k + 3] * inv);
             if (direct) {  // bf16, as the queries of this kernel are
-              uint16_t* dst = static_cast<uint16_t*>(p.out.ptr) + orow * p.out.row_stride + h * p.out.head_stride;
-              *reinterpret_cast<uint4*>(dst + 32 * c + j) = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[0].z, v[0].w),
-                                                                      pack_bf16(v[1].x, v[1].y), pack_bf16(v[1].z, v[1].w));
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out.ptr) + off + 32 * c + j) =
+                  make_uint4(pack_bf16(o[j], o[j + 1]), pack_bf16(o[j + 2], o[j + 3]), pack_bf16(o[j + 4], o[j + 5]),
+                             pack_bf16(o[j + 6], o[j + 7]));
             } else {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) *reinterpret_cast<float4*>(p.part_o + pr * D + 32 * c + j + 4 * k) = v[k];
+              float4* dst = reinterpret_cast<float4*>(p.part_o + pr * D + 32 * c + j);
+              dst[0] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+              dst[1] = make_float4(o[j + 4], o[j + 5], o[j + 6], o[j + 7]);
             }
           }
         }
