@@ -30,14 +30,15 @@
 // so that the error of a weight cancels where one token holds most of it; the log-sum-exp,
 // when asked for, is summed over the unrounded ones.
 //
-// Measured: 64 new tokens over 131072 cached ones, 32 heads on 8, 180 us (its products take 89
+// Measured: 64 new tokens over 131072 cached ones, 32 heads on 8, 171 us (its products take 89
 // at the rate of a large matrix product); 32 over 64 x 4096 in 2-bit values, 28 heads on 4,
-// 233 us (78).  The exponential units are 44 % busy, the tensor pipe 46 %, the issue slots 51 %;
-// what bounds the kernel is that a tile
-// passes five hand-overs (decoder, logits, weights, readout, release), each some 150 cycles
-// even when nothing is left to wait for: without exponentials, products and loads they alone
-// take 104 us of the 180.  More warps on the softmax (193), lanes in ping-pong (231) and one
-// row block per CTA with three logit buffers (201) were slower.
+// 218 us (78).  The exponential units are 46 % busy, the tensor pipe 48 %, the issue slots
+// 53 %; what bounds the kernel is that a tile passes five hand-overs (decoder, logits, weights,
+// readout, release), each some 150 cycles even when nothing is left to wait for: without
+// exponentials, products and loads they alone take 104 us of the long case.  Measured while
+// that stood at 180: sixteen softmax warps 193, lanes in ping-pong 231, one row block per CTA
+// with three logit buffers 201.  A CTA's set-up, first tile and outputs are some 8 us; the
+// kernel therefore starts on the cache while the queries are still being prepared.
 //
 // TMEM (512 columns): logits of lane l at 128 l (its weights overwrite them, two to a
 // column), outputs at 256 + 128 l.
