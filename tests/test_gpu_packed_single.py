@@ -1,4 +1,4 @@
-"""headq_tree_attn of single tokens, and one workspace under calls of many sizes."""
+"""headq_tree_attn of single tokens, one workspace under calls of many sizes, calls in a row."""
 
 import numpy as np
 import pytest
@@ -269,3 +269,40 @@ def test_offsets_past_32_bits(vmode, B):
         cu[B] = n
         got = hq().headq_tree_attn(big, q, U0, cu=cu, n=n, sm_scale=1.0)
         check_tree(got, None, ref_tree(one, q, [n], [512], None, sm=1.0, sigma=0.0))
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,r,n,vmode,qd", [
+    (12, 12, 64, 8, 11, "dense", BF), (28, 4, 128, 16, 32, "dense", BF), (28, 4, 128, 16, 32, "2bit", BF),
+    (28, 4, 128, 16, 1, "dense", BF), (8, 2, 128, 16, 7, "dense", F32), (4, 4, 64, 0, 3, "dense", BF)])
+def test_steps_in_a_row_on_one_workspace(Hq, Hkv, d, r, n, vmode, qd):
+    """Write, attend, read, over and over with nothing between: the kernels of a step that start
+    early see the cache, queries and workspace as the steps before them left these."""
+    B, T, steps = 3, 2048, 24
+    rng = np.random.default_rng(n)
+    kvs = [torch.from_numpy(rng.standard_normal((B * n, 2 * Hkv, d)).astype(np.float32)).cuda().to(BF)
+           for _ in range(steps)]
+    qs = [torch.from_numpy(rng.standard_normal((B * n, Hq, d)).astype(np.float32)).cuda().to(qd) for _ in range(steps)]
+    lens = [torch.tensor([T - 3 * k, n + 5 * k, 700 + k], dtype=torch.int32, device="cuda") for k in range(steps)]
+
+    def run(sync):
+        c = Cache(61, B, Hkv, T, d, r, vmode)
+        ws = hq().tree_workspace(c.hq, Hq, n)
+        q, kv, sl = torch.empty_like(qs[0]), torch.empty_like(kvs[0]), torch.empty_like(lens[0])
+        outs, rows = [], []
+        for k in range(steps):
+            q.copy_(qs[k])
+            kv.copy_(kvs[k])
+            sl.copy_(lens[k])
+            hq().headq_cache_write_ragged(c.hq, kv[:, :Hkv], kv[:, Hkv:], c.U, seq_lens=sl, n=n)
+            outs.append(hq().headq_tree_attn(c.hq, q, c.U, seq_lens=sl, n=n, ws=ws))
+            rows.append(hq().headq_cache_read(c.hq, c.U, seq_lens=sl, n=n))
+            if sync:
+                torch.cuda.synchronize()
+        hq().headq_workspace_status(ws)
+        return outs, rows
+
+    a, b = run(True), run(False)
+    for x, y in zip(a[0], b[0]):
+        assert torch.equal(x, y)
+    for (k0, v0), (k1, v1) in zip(a[1], b[1]):
+        assert torch.equal(k0, k1) and torch.equal(v0, v1)
