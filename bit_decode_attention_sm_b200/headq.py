@@ -579,31 +579,33 @@ def _rows(t, name, heads, d, written=False):
     multiples of 16 bytes, channels contiguous; elements of a written one do not overlap."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError("%s must be [rows, %d, %d], got %s" % (name, heads, d, list(t.shape)))
-    code = _dtype_code(t)
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError("%s must be [rows, %d, %d], got %s" % (name, heads, d, list(shape)))
+    rows, code = shape[0], _dtype_code(t)
     rs, hs, cs = t.stride()
     per = 4 if code == HEADQ_F32 else 8
-    if t.shape[0] <= 1:  # the strides of a single row or head are never used
+    if rows <= 1:  # the strides of a single row or head are never used
         rs = 0
     if heads == 1:
         hs = 0
     if cs != 1 or rs % per or hs % per:
         raise ValueError("%s: channels must be contiguous and the other strides multiples of 16 bytes"
                          % name)
-    if written and t.shape[0] > 1 and heads > 0:
-        lo, hi = sorted(((rs, t.shape[0]), (hs, heads))) if heads > 1 else ((d, 1), (rs, t.shape[0]))
-        if lo[0] < d or hi[0] < (lo[1] - 1) * lo[0] + d:
+    if written and not (rs >= heads * hs >= heads * d):  # not the plain order: what lies inside what
+        if rows > 1 and heads > 0:
+            lo, hi = sorted(((rs, rows), (hs, heads))) if heads > 1 else ((d, 1), (rs, rows))
+            if lo[0] < d or hi[0] < (lo[1] - 1) * lo[0] + d:
+                raise ValueError("%s: its rows and heads overlap" % name)
+        elif heads > 1 and hs < d:
             raise ValueError("%s: its rows and heads overlap" % name)
-    elif written and heads > 1 and hs < d:
-        raise ValueError("%s: its rows and heads overlap" % name)
     return RowsStruct(t.data_ptr(), code, rs, hs)
 
 
 def _int32(t, name, shape):
     if t is None:
         return None
-    if _cuda(t, name).dtype != torch.int32 or tuple(t.shape) != shape:
+    if _cuda(t, name).dtype != torch.int32 or t.shape != shape:
         raise ValueError("%s must be int32 %s" % (name, list(shape)))
     return t.data_ptr()
 
@@ -623,7 +625,7 @@ def _span(cache, seq_lens, cu, n, T, rows):
 def _basis(cache, U):
     if cache.r == 0:
         return None
-    if _cuda(U, "U") is None or U.dtype != torch.float32 or tuple(U.shape) != (cache.Hkv, cache.d, cache.r):
+    if _cuda(U, "U") is None or U.dtype != torch.float32 or U.shape != (cache.Hkv, cache.d, cache.r):
         raise ValueError("U must be float32 [%d, %d, %d]" % (cache.Hkv, cache.d, cache.r))
     return U.data_ptr()
 
