@@ -759,6 +759,9 @@ decode_mma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap vmap
         Ls = fmaf(f, ml[w * GM + h], Ls);
       }
       if constexpr (V2) O += mo[h * D + c];  // sum_j p_j scale_{j,g} code_{j,c}, relative to M
+    } else {  // nothing seen; or sums that are not numbers, which the maximum passes over: kept
+#pragma unroll
+      for (int w = 0; w < kCW; ++w) Ls += ml[w * GM + h];
     }
     const size_t bh = static_cast<size_t>(b) * p.Hq + h0 + h;
     if (single) {
