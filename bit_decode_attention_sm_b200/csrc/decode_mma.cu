@@ -766,7 +766,7 @@ decode_mma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap vmap
     const size_t bh = static_cast<size_t>(b) * p.Hq + h0 + h;
     if (single) {
       p.out[bh * D + c] = Ls > 0.f ? O / Ls : 0.f;
-      if (c == 0 && p.lse) p.lse[bh] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+      if (c == 0 && p.lse) p.lse[bh] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : empty_lse(p, Ls);
     } else if (!failed) {
       pv.o[(bh * p.splits + split) * D + c] = O;
       if (c == 0) {

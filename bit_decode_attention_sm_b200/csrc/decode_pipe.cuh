@@ -240,7 +240,7 @@ __device__ __forceinline__ void merge_splits_last(const DecodeParams& p, int b, 
       r.w = ((acc[0].w + acc[1].w) + (acc[2].w + acc[3].w)) * inv;
       reinterpret_cast<float4*>(p.out + bh * D)[lane] = r;
     }
-    if (lane == 0 && p.lse) p.lse[bh] = ls > 0.f ? mx + logf(ls) : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[bh] = ls > 0.f ? mx + logf(ls) : empty_lse(p, ls);
   }
 }
 

@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "headq.h"
@@ -214,7 +215,14 @@ struct DecodeParams {
   bool new_bf16;
   float* out;
   float* lse;
+  bool nan_lse;  // see empty_lse
 };
+
+// The log-sum-exp of a row whose sum of weights L is not positive (its output is 0): minus
+// infinity; on request a sum that is not a number is passed on.
+__device__ __forceinline__ float empty_lse(const DecodeParams& p, float L) {
+  return p.nan_lse && L != L ? L : -INFINITY;
+}
 
 struct AttnKlParams {
   headq_cache c;

@@ -295,8 +295,8 @@ tree_one_prep_kernel(const TreeParams p, const TreeOne w) {
   }
 }
 
-// Their results to the packed rows.  The decode kernels give 0 and -inf for a sum of weights
-// that is not positive, not-a-number included; here only a row that sees nothing has that.
+// Their results to the packed rows.  The decode kernels give 0 for a sum of weights that is not
+// positive; one that is not a number reaches the log-sum-exp (nan_lse) and makes the row NaN.
 __global__ void __launch_bounds__(256)
 tree_one_finish_kernel(const TreeParams p, const TreeOne w) {
   const int b = blockIdx.x, tid = threadIdx.x;
@@ -304,15 +304,13 @@ tree_one_finish_kernel(const TreeParams p, const TreeOne w) {
   if (sq.n == 0) return;
   const int per = p.c.d / 4;
   const size_t r0 = static_cast<size_t>(b) * p.Hq;
-  const bool sees = w.lens[b] > 0;
   for (int e = tid; e < p.Hq * per; e += 256) {
     const int h = e / per, c4 = e - h * per;
     float4 o = reinterpret_cast<const float4*>(w.out)[r0 * per + e];
     const float lse = w.lse[r0 + h];
-    const bool nan = sees && lse == -INFINITY;
-    if (nan) o.x = o.y = o.z = o.w = NAN;
+    if (lse != lse) o.x = o.y = o.z = o.w = NAN;
     store_row4(p.out, sq.row0 * p.out.row_stride + h * p.out.head_stride + 4 * c4, o);
-    if (p.lse && c4 == 0) p.lse[static_cast<size_t>(sq.row0) * p.Hq + h] = nan ? NAN : lse;
+    if (p.lse && c4 == 0) p.lse[static_cast<size_t>(sq.row0) * p.Hq + h] = lse;
   }
 }
 
@@ -421,6 +419,7 @@ cudaError_t launch_tree_one(const TreeParams& p, const TreeOne& w, cudaStream_t 
   d.part = w.part;
   d.out = w.out;
   d.lse = w.lse;
+  d.nan_lse = true;
   if ((e = launch_decode(d, dp.mma, s)) != cudaSuccess) return e;
   tree_one_finish_kernel<<<p.c.B, 256, 0, s>>>(p, w);
   return cudaGetLastError();

@@ -459,7 +459,8 @@ headq_status headq_cache_read(const headq_cache *cache, const headq_span *span, 
  *   out[row, h] = sum_j softmax(s^)_j v^_j ,  lse[row, h] = log sum_j exp(s^_j)
  * over the tokens it sees, as headq_decode_attn computes them for a path through the
  * tree: what a token's keys and values hold does not reach a row that does not see it.
- * A row that sees nothing gets out = 0, lse = -inf.
+ * A row that sees nothing, or only tokens with logits of minus infinity, gets out = 0,
+ * lse = -inf.
  *   q     [rows, Hq, d];  out  [rows, Hq, d] of q's dtype;  lse fp32 [rows, Hq] (nullable)
  *   mask  uint8 [n, n] of sequence b at mask + b * mask_stride bytes, row i column j
  *         nonzero when new token i sees new token j (mask_stride 0: one tree for all).

@@ -59,3 +59,32 @@ def test_a_split_of_tokens_that_are_not_numbers_is_felt(i, name):
     # the decode call itself: no row with such a token passes for a finite one
     o, l = hq().headq_decode_attn(c.hq, q, c.U, seq_lens=lens_of(lens))
     assert not torch.isfinite(l[:2]).any() and torch.isfinite(o[2]).all() and torch.isfinite(l[2]).all()
+
+
+# ---------------------------------------------------------------- far from zero
+
+FORMS = [  # Hq, Hkv, d, r, vmode, n, query dtype: every kernel of the tree attention
+    (8, 2, 128, 16, "dense", 1, BF), (2, 2, 64, 8, "2bit", 1, BF), (14, 2, 128, 16, "dense", 1, BF),
+    (10, 2, 64, 8, "2bit", 1, BF), (8, 2, 128, 16, "dense", 3, BF), (14, 2, 64, 8, "2bit", 40, BF),
+    (8, 2, 128, 16, "dense", 2, F32), (4, 2, 32, 0, "2bit", 1, BF),
+]
+
+
+def same_keys(c, x):
+    """Every cached key has `x` in all channels, without a side code."""
+    c.planes["k_scale"].zero_()
+    c.planes["k_min"].fill_(x)
+    if c.r:
+        c.planes["z_scale"].zero_()
+
+
+@pytest.mark.parametrize("i", range(len(FORMS)))
+def test_rows_whose_logits_are_all_minus_infinity(i):
+    """q . k beyond the range of fp32: such a row gives 0 and minus infinity in every form."""
+    Hq, Hkv, d, r, vmode, n, qd = FORMS[i]
+    c = Cache(90 + i, 2, Hkv, 512, d, r, vmode)
+    same_keys(c, -1e25)
+    q = torch.full((2 * n, Hq, d), 1e25, device="cuda", dtype=qd)
+    lse = torch.zeros(2 * n, Hq, device="cuda")
+    out = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=lens_of([500, n]), n=n, lse=lse)
+    assert (out == 0).all() and (lse == -np.inf).all()
