@@ -59,7 +59,7 @@ constexpr int kGM = 8;                    // head slots
 constexpr int kCT = kCW * 32;             // consumer threads
 constexpr float kRescale = 8.0f;          // log2 units the stale max may lag (p <= 2^8)
 constexpr int kRaiseLog2 = 12;            // 2-bit values: entries stay below 2^(E + 12)
-constexpr float kMaxInit = -1e30f;        // running max before the first logit (finite)
+constexpr float kMaxInit = -0x1.FFFFFEp127f;  // running max before the first logit: the lowest finite number
 
 // pipeline depth (the stages also hold the merging CTA's [G][splits] weights)
 // and CTAs per SM: two, with registers for the operand fragments, the output

@@ -88,3 +88,25 @@ def test_rows_whose_logits_are_all_minus_infinity(i):
     lse = torch.zeros(2 * n, Hq, device="cuda")
     out = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=lens_of([500, n]), n=n, lse=lse)
     assert (out == 0).all() and (lse == -np.inf).all()
+
+
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("i", [i for i in range(len(FORMS)) if FORMS[i][5:] == (1, BF)])
+def test_rows_whose_logits_are_equal_and_huge(i, sign):
+    """Equal logits near -1e34 or 1e34: the mean of the values that a row sees."""
+    Hq, Hkv, d, r, vmode, n, qd = FORMS[i]
+    c = Cache(90 + i, 2, Hkv, 512, d, r, vmode)
+    same_keys(c, sign * 2.0 ** 50)
+    q = torch.full((2 * n, Hq, d), 2.0 ** 60, device="cuda", dtype=qd)
+    lens = [500, n]
+    lse = torch.zeros(2 * n, Hq, device="cuda")
+    out = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=lens_of(lens), n=n, lse=lse)
+    v = c.parts()[2]
+    logit = sign * 2.0 ** 110 * np.sqrt(d)
+    for b in range(2):
+        for j in range(n):
+            m = v[b, :, :lens[b] - n + j + 1].mean(1)                    # [Hkv, d]
+            got = out[b * n + j].double().cpu().numpy().reshape(Hkv, -1, d)
+            # equal weights are exact powers of two or fp32 numbers; values to bf16, then the output
+            assert (np.abs(got - m[:, None]) <= 2.0 ** -6 * (np.abs(m[:, None]) + 0.1)).all()
+    assert (np.abs(lse.double().cpu().numpy() / logit - 1) <= 2.0 ** -18).all()
