@@ -518,8 +518,10 @@ __device__ __forceinline__ RowState raise_max(RowState st, float top, uint32_t t
 constexpr int kHalf = kTile / 2;
 
 // The logits of half a tile that holds new tokens or ends the sequence, in TMEM: each token
-// has its own scale, and is masked.  a: new-token index of the half's first token.
-__device__ __forceinline__ void mask_half(uint32_t ts, const uint32_t* row, int wpr, int i, int a, const float* col) {
+// has its own scale, and is masked.  a: new-token index of the half's first token; f: the row's
+// factor to log2 units.
+__device__ __forceinline__ void mask_half(uint32_t ts, const uint32_t* row, int wpr, int i, int a, const float* col,
+                                          float f) {
 #pragma unroll 1
   for (int c = 0; c < kHalf; c += 16) {
     uint32_t w[16];
@@ -528,7 +530,7 @@ __device__ __forceinline__ void mask_half(uint32_t ts, const uint32_t* row, int 
     tc_wait_ld();
 #pragma unroll
     for (int j = 0; j < 16; ++j)
-      w[j] = __float_as_uint((bits >> j) & 1u ? __uint_as_float(w[j]) * col[c + j] : -INFINITY);
+      w[j] = __float_as_uint((bits >> j) & 1u ? __uint_as_float(w[j]) * col[c + j] * f : -INFINITY);
     tc_st16(ts + c, w, 0);
   }
   tc_wait_st();
@@ -556,6 +558,12 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[kHalf], float f, flo
   sum = codec::pk_lo(t) + codec::pk_hi(t);
   bits = any[0] | any[1];
 }
+
+// Once a row of a warp reaches logits of this size (log2 units), its logits are rounded before
+// the maximum is taken off.  weights() takes it off the unrounded product; the maximum itself is
+// rounded, which leaves up to half a unit in its last place in every exponent: it cancels in the
+// quotient, but passes the range of fp32 when the logits reach 2^32.
+constexpr float kBigLogit = 0x1p24f;
 
 // The sum of channel `ch` over the new tokens that row i sees and whose value there is not
 // finite once rounded to bf16 (they were left out of the value tiles).
@@ -897,7 +905,8 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
     // weights are written.
     uint32_t s[kHalf];
     float f = 0.0f;
-    const int tail_at = min(P, t_hi) >= t_lo ? (min(P, t_hi) - t_lo) / kTile : 0;  // tiles from here on hold new tokens or end the sequence
+    // tiles from here on hold new tokens or end the sequence, or have logits to be rounded (kBigLogit)
+    int round_from = min(P, t_hi) >= t_lo ? (min(P, t_hi) - t_lo) / kTile : 0;
 #pragma unroll 1
     for (int y = -1; y < 2 * nk && ok; ++y) {  // step y: half y & 1 of the lane's tile y / 2
       const int h = y & 1;
@@ -916,6 +925,12 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
           // (ok stays the same in a whole warp, which works together to the end)
           if (y > 0) ok = __all_sync(kAll, ok && mbar_wait(o_done(wl, 1 - h), ((y - 1) >> 1) & 1));
           tc_fence_after();
+          if (__any_sync(kAll, fabsf(top) >= kBigLogit && top != -INFINITY)) {
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * f);
+            f = 1.0f;
+            round_from = 0;
+          }
           st = raise_max<D>(st, top > st.m ? top + kSlack : st.m, to, y > 0);
           weights(s, f, st.m, w, sum, bits);
         }
@@ -947,9 +962,10 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         const uint32_t sa = ts + kHalf * (1 - h);
         tc_fence_after();
         f = fmaxf(fq * col[0], 1e-37f);
-        if (tile >= tail_at) {
-          f = fmaxf(fq, 1e-37f);
-          mask_half(sa, words, t.wpr, i, t_lo + tile * kTile + kHalf * (1 - h) - P, col + kHalf * (1 - h));
+        if (tile >= round_from) {
+          mask_half(sa, words, t.wpr, i, t_lo + tile * kTile + kHalf * (1 - h) - P, col + kHalf * (1 - h),
+                    fmaxf(fq, 1e-37f));
+          f = 1.0f;
         }
         tc_ld32(sa, s, 0);
         tc_ld32(sa + 32, s, 32);
