@@ -66,8 +66,12 @@ constexpr int kKStages = 2;
 constexpr int kRing = 8;            // tiles whose key scales are kept (more than can be in flight)
 // A row's weights are 2^(logit - m) with m at least the largest logit so far and, when it is
 // set, kSlack above it: the check that a step stays below 2 is then one bit of the weights,
-// and m is seldom set again.  Weights, sums and accumulators all have the 8-bit exponent of
-// fp32, so the offset costs no precision (a weight 2^-66 of the largest is still normal).
+// and m is seldom set again.  Weights and sums have the 8-bit exponent of fp32, so the offset
+// costs them no precision (a weight 2^-66 of the largest is still normal).  It does cost the
+// readout's range: weight * value with the largest weight near 2^-60 is subnormal for values
+// below 2^-66, which lose their last bits, and 0 below 2^-89.  Smaller offsets were slower where
+// logits spread: 2^40 233-237 us on the full-KV 2-bit layer, 2^30 248-260, 2^20 279-288 (2^60
+// 226-229).
 constexpr float kSlack = 60.0f;
 constexpr uint32_t kAll = 0xffffffffu;
 

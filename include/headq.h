@@ -470,9 +470,11 @@ headq_status headq_cache_read(const headq_cache *cache, const headq_span *span, 
  *         first word is the device error word.  Calls sharing it must not overlap on the GPU.
  * bf16 q with bf16 or 2-bit values, d 64 or 128 and r 0, 8 or 16 runs on the tensor cores:
  * keys are rounded to 11 bits relative to the largest of their tile and softmax weights
- * to bf16, so out carries about 2 roundings to bf16.  Of those, calls with n = 1 and
- * Hq / Hkv <= 8 run the kernels of headq_decode_attn.  Every other shape, and fp32 q, is
- * computed in fp32.  HEADQ_K_TOKEN caches only.
+ * truncated to bf16 (and summed as truncated), so out carries about 2 roundings to bf16; values below 2^-66 in size lose bits as
+ * subnormal numbers do, and below 2^-89 count as 0.  Of those, calls with n = 1 and
+ * Hq / Hkv <= 8 run the kernels of headq_decode_attn (but for 2-bit values with r = 0, and
+ * for B * Hkv > 8192).  Every other shape, and fp32 q, is computed in fp32.  HEADQ_K_TOKEN
+ * caches only.
  */
 headq_status headq_tree_attn(const headq_cache *cache, const headq_rows *q, int Hq,
                              const uint8_t *mask, long long mask_stride, const headq_span *span,

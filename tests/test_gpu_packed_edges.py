@@ -119,3 +119,44 @@ def test_rows_whose_logits_are_equal_and_huge(i, sign):
                 tol = tol + (2.0 ** -11 + 512 * 2.0 ** -23) * steps + 512 * 2.0 ** -23 * (a + steps)
             assert (np.abs(got - m) <= tol).all()
     assert (np.abs(lse.double().cpu().numpy() / logit - 1) <= 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("e", [-100, -60, 60, 120])
+@pytest.mark.parametrize("i", range(len(FORMS)))
+def test_keys_and_queries_of_opposite_magnitudes(i, e):
+    """Keys times 2^e against queries times 2^-e: the same logits, whatever either's size."""
+    Hq, Hkv, d, r, vmode, n, qd = FORMS[i]
+    c = Cache(130 + i, 2, Hkv, 512, d, r, vmode)
+    rng = np.random.default_rng(i)
+    q = torch.from_numpy(rng.standard_normal((2 * n, Hq, d)).astype(np.float32) * 1.5).cuda().to(qd)
+    lens = [500, 300]
+    ref = ref_tree(c, q, [n, n], lens, None)
+    for name in ("k_scale", "k_min", "z_scale"):
+        if name in c.planes:
+            c.planes[name] *= 2.0 ** e
+    q = (q.float() * 2.0 ** -e).to(qd)
+    lse = torch.zeros(2 * n, Hq, device="cuda")
+    out = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=lens_of(lens), n=n, lse=lse)
+    check_tree(out, lse, ref)
+
+
+@pytest.mark.parametrize("mag", [1e-27, 2.0 ** -64, 1e-9, 1e9, 1e30])
+@pytest.mark.parametrize("i", range(len(FORMS)))
+def test_value_magnitudes(i, mag):
+    """Values far from 1 keep their relative precision: from 2^-66 up where several tokens run
+    on the tensor cores, everywhere else in every form."""
+    Hq, Hkv, d, r, vmode, n, qd = FORMS[i]
+    if mag < 2.0 ** -66 and n > 1 and qd == BF:
+        return
+    c = Cache(100 + i, 2, Hkv, 512, d, r, vmode)
+    for name in ("v", "v_scale", "v_min"):
+        if name in c.planes:
+            c.planes[name].copy_(c.planes[name].float() * mag)
+    rng = np.random.default_rng(i)
+    q = torch.from_numpy(rng.standard_normal((2 * n, Hq, d)).astype(np.float32)).cuda().to(qd)
+    lens = [500, 300]
+    out = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=lens_of(lens), n=n)
+    assert out.abs().max() > 0.01 * mag
+    ref = ref_tree(c, q, [n, n], lens, None)
+    # in units of the magnitude, so that the tolerances' absolute parts stay negligible
+    check_tree(out.double() / mag, None, [ref[0] / mag, None, (ref[2] - 1e-30) / mag + 1e-30, None])
