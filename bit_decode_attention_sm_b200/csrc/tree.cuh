@@ -70,12 +70,10 @@ __device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int i, int
   return p.mask ? p.mask[b * p.mask_stride + static_cast<long long>(i) * p.span.n + j] != 0 : j <= i;
 }
 
-// 4 channels of a 2-bit code: min + code * scale
+// 4 channels of a 2-bit code: min + code * scale, the product rounded before the sum
 __device__ __forceinline__ float4 decode4(uint32_t byte, float scale, float mn) {
-  return make_float4(fmaf(static_cast<float>(byte & 3u), scale, mn),
-                     fmaf(static_cast<float>((byte >> 2) & 3u), scale, mn),
-                     fmaf(static_cast<float>((byte >> 4) & 3u), scale, mn),
-                     fmaf(static_cast<float>((byte >> 6) & 3u), scale, mn));
+  auto at = [&](int k) { return __fadd_rn(__fmul_rn(static_cast<float>((byte >> (2 * k)) & 3u), scale), mn); };
+  return make_float4(at(0), at(1), at(2), at(3));
 }
 
 // 4 channels of an output row, rounded to its dtype

@@ -440,7 +440,8 @@ headq_status headq_cache_write_ragged(const headq_cache *cache, const headq_rows
  * headq_cache_read -- decode cached tokens to dense rows (summary section 3: the key
  * the corrected logit reads, and the cached value):
  *   k_out[row, kv] = k^base + corr_sign * U_h z^ ,  v_out[row, kv] = v^
- * computed in fp32 and rounded once to the rows' dtype.  k_out or v_out may be NULL.
+ * computed in fp32 and rounded once to the rows' dtype (in fp32 rows k^base and 2-bit v^
+ * are min + code * scale with the product rounded first, as the write has them).  k_out or v_out may be NULL.
  * Any interval [a, e) of a sequence is the span with T_b = e and n_b = e - a.  Both key
  * codes are supported.  A block-table entry outside the page pool gives zero rows, and
  * sets the error word of `ws` when there is one (ws nullable: any zero-filled decode or

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from packed_helpers import Cache, check_tree, ref_tree
+from packed_helpers import Cache, check_tree, logical, ref_tree
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -160,3 +160,45 @@ def test_value_magnitudes(i, mag):
     ref = ref_tree(c, q, [n, n], lens, None)
     # in units of the magnitude, so that the tolerances' absolute parts stay negligible
     check_tree(out.double() / mag, None, [ref[0] / mag, None, (ref[2] - 1e-30) / mag + 1e-30, None])
+
+
+# ---------------------------------------------------------------- dequantised, bit for bit
+
+@pytest.mark.parametrize("kmode", ["token", "channel"])
+@pytest.mark.parametrize("d,r,page", [(128, 16, 0), (64, 8, 64), (128, 0, 0), (32, 4, 0)])
+def test_read_rounds_the_product_before_the_sum(d, r, page, kmode):
+    """Base keys and 2-bit values read in fp32 are min + code * scale with the product rounded
+    first, as the write forms them when it takes the residual."""
+    c = Cache(110, 2, 3, 128, d, r, "2bit", F32, page, kmode)
+    ch = np.arange(d)
+    gs = min(32, d)
+
+    def base(codes, scale, mn, channel):
+        c8 = logical(codes, c.table).cpu().numpy()
+        s, m = (logical(x, c.table).cpu().numpy() for x in (scale, mn))
+        code = ((c8[..., ch // 4] >> (2 * (ch % 4))) & 3).astype(np.float32)
+        if channel:
+            blk = np.arange(128) // 64
+            return m[:, :, blk] + (code * s[:, :, blk]).astype(np.float32)
+        return m[..., ch // gs] + (code * s[..., ch // gs]).astype(np.float32)
+
+    p = c.planes
+    k = base(p["k_codes"], p["k_scale"], p["k_min"], kmode == "channel")
+    v = base(p["v_codes"], p["v_scale"], p["v_min"], False)
+    # keys and values by CTAs of their own, and in one CTA
+    for kw in (dict(), dict(k_out=0), dict(v_out=0)):
+        kw = {n: torch.empty(256, 3, d, device="cuda") for n in kw}
+        kg, vg = hq().headq_cache_read(c.hq, c.U, n=128, corr_sign=0, dtype=F32, **kw)
+        for got, want in ((kg, k), (vg, v)):
+            if got is not None:
+                assert np.array_equal(got.cpu().numpy(), want.transpose(0, 2, 1, 3).reshape(256, 3, d))
+
+
+@pytest.mark.parametrize("d,r", [(128, 16), (64, 8), (32, 4)])
+def test_a_lone_token_is_its_value(d, r):
+    """fp32 queries that see one token: its dequantised value, bit for bit."""
+    c = Cache(111, 5, 3, 64, d, r, "2bit")
+    q = torch.randn(5, 6, d, generator=torch.Generator().manual_seed(1)).cuda()
+    out = hq().headq_tree_attn(c.hq, q, c.U, T=1)
+    v = hq().headq_cache_read(c.hq, c.U, n=1, T=1, dtype=F32)[1]
+    assert torch.equal(out, v.repeat_interleave(2, 1))
