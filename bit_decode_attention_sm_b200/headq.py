@@ -253,6 +253,8 @@ class HeadQCache:
         c.v_dtype = torch.bfloat16 if v is None else v.dtype
         c.k_codes, c.k_scale, c.k_min, c.z_codes, c.z_scale = k_codes, k_scale, k_min, z_codes, z_scale
         c.v, c.v_codes, c.v_scale, c.v_min = v, v_codes, v_scale, v_min
+        if block_table is not None:
+            c._table()
         return c
 
     def planes(self):
@@ -274,6 +276,15 @@ class HeadQCache:
             b += self.d * (2 if self.v_dtype == torch.bfloat16 else 4)
         return b
 
+    def _table(self):
+        """The block table, as the kernels index it; it may have been assigned since the last call."""
+        t = self.block_table
+        if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous()
+                or t.shape != (self.B, self.max_pages) or t.device != self.k_codes.device):
+            raise ValueError("block_table must be contiguous int32 [%d, %d] on %s"
+                             % (self.B, self.max_pages, self.k_codes.device))
+        return t
+
     def struct(self):
         s = CacheStruct()
         s.B, s.Hkv, s.T_cap, s.d, s.r = self.B, self.Hkv, self.T_cap, self.d, self.r
@@ -293,7 +304,7 @@ class HeadQCache:
             s.v_min = self.v_min.data_ptr()
         if self.page_size:
             s.page_size, s.num_pages, s.max_pages = self.page_size, self.num_pages, self.max_pages
-            s.block_table = self.block_table.data_ptr()
+            s.block_table = self._table().data_ptr()
         s.kmode = KMODES[self.kmode]
         return s
 

@@ -1,0 +1,38 @@
+"""Checks of the Python binding's arguments, on a machine without a GPU."""
+
+import pytest
+import torch
+
+from test_abi_host import hq  # noqa: F401  (the fixture)
+
+
+def paged(hq, **kw):
+    return hq.PagedHeadQCache(2, 4, 128, 16, 128, 9, 3, device="cpu", **kw)
+
+
+@pytest.mark.parametrize("table", [
+    torch.zeros(2, 3, dtype=torch.int64),                       # read as pairs of words
+    torch.zeros(2, 2, dtype=torch.int32),                       # too short for max_pages
+    torch.zeros(1, 3, dtype=torch.int32),                       # a sequence is missing
+    torch.zeros(6, dtype=torch.int32),
+    torch.zeros(2, 6, dtype=torch.int32)[:, ::2],               # strided
+    torch.zeros(2, 3, dtype=torch.int32, device="meta"),        # on another device than the planes
+    [[0, 1, 2], [3, 4, 5]],
+], ids=["int64", "pages", "sequences", "flat", "strided", "device", "list"])
+def test_an_assigned_block_table_is_checked(hq, table):
+    c = paged(hq)
+    c.struct()
+    c.block_table = table
+    with pytest.raises(ValueError, match="block_table"):
+        c.struct()
+
+
+def test_from_planes_checks_the_table(hq, monkeypatch):
+    """As for every other plane: the table lies on the planes' device."""
+    monkeypatch.setattr(hq, "_cuda", lambda t, name: t)
+    p = dict(k_codes=torch.zeros(9, 4, 128, 32, dtype=torch.uint8), k_scale=torch.zeros(9, 4, 128, 4),
+             k_min=torch.zeros(9, 4, 128, 4), v=torch.zeros(9, 4, 128, 128))
+    ok = torch.zeros(2, 3, dtype=torch.int32)
+    assert hq.HeadQCache.from_planes(block_table=ok, **p).max_pages == 3
+    with pytest.raises(ValueError, match="block_table"):
+        hq.HeadQCache.from_planes(block_table=ok.to("meta"), **p)
