@@ -621,6 +621,14 @@ def _int32(t, name, shape):
     return t.data_ptr()
 
 
+def _int(x, name):
+    """x as the C structures hold it; ctypes would wrap a larger one."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError("%s = %d does not fit 32 bits" % (name, x))
+    return x
+
+
 def _span(cache, seq_lens, cu, n, T, rows):
     """``headq_span`` of a packed batch of `rows` rows."""
     if n is None:
@@ -630,7 +638,7 @@ def _span(cache, seq_lens, cu, n, T, rows):
             raise ValueError("%d rows are no whole number for each of %d sequences" % (rows, cache.B))
         n = rows // cache.B if cache.B else 0
     return SpanStruct(_int32(seq_lens, "seq_lens", (cache.B,)), _int32(cu, "cu", (cache.B + 1,)),
-                      cache.T_cap if T is None else int(T), int(n), rows)
+                      cache.T_cap if T is None else _int(T, "T"), _int(n, "n"), _int(rows, "rows"))
 
 
 def _basis(cache, U):
@@ -692,8 +700,9 @@ def tree_workspace(cache, Hq, n, T=None, stream=None):
     """A zeroed device workspace for headq_tree_attn with up to n new tokens per sequence and
     lengths up to T (None: the capacity)."""
     cs = cache.struct()
+    n, T = _int(n, "n"), cache.T_cap if T is None else _int(T, "T")
     with torch.cuda.device(cache.k_codes.device):
-        nb = lib().headq_tree_workspace_bytes(cs, Hq, int(n), cache.T_cap if T is None else int(T))
+        nb = lib().headq_tree_workspace_bytes(cs, Hq, n, T)
     return _zeros(max(nb, 256), torch.uint8, cache.k_codes.device, stream)
 
 

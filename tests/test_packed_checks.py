@@ -1,5 +1,7 @@
 """Checks of the Python binding's arguments, on a machine without a GPU."""
 
+import types
+
 import pytest
 import torch
 
@@ -36,3 +38,18 @@ def test_from_planes_checks_the_table(hq, monkeypatch):
     assert hq.HeadQCache.from_planes(block_table=ok, **p).max_pages == 3
     with pytest.raises(ValueError, match="block_table"):
         hq.HeadQCache.from_planes(block_table=ok.to("meta"), **p)
+
+
+@pytest.mark.parametrize("kw", [dict(n=2 ** 32 + 1), dict(n=2 ** 31), dict(n=-2 ** 31 - 1), dict(T=2 ** 32 + 5),
+                                dict(rows=2 ** 32 + 2)])
+def test_sizes_past_32_bits_are_refused(hq, kw):
+    """They would wrap to other sizes in the C structures."""
+    c = types.SimpleNamespace(B=2, T_cap=64)
+    args = dict(seq_lens=None, cu=None, n=1, T=None, rows=2)
+    hq._span(c, **args)
+    with pytest.raises(ValueError, match="32 bits"):
+        hq._span(c, **{**args, **kw})
+    kw.pop("rows", None)
+    if kw:
+        with pytest.raises(ValueError, match="32 bits"):
+            hq.tree_workspace(paged(hq), 4, kw.get("n", 1), kw.get("T"))
