@@ -749,4 +749,7 @@ def headq_tree_attn(cache, q, U, mask=None, seq_lens=None, cu=None, n=None, T=No
 
 def headq_workspace_status(ws, stream=None):
     """Synchronises and raises HeadQError if a kernel flagged a device-side error."""
-    _check("headq_workspace_status", lib().headq_workspace_status(_ptr(ws), _stream(stream)))
+    s = torch.cuda.current_stream(ws.device) if stream is None else stream
+    with torch.cuda.device(ws.device):
+        _check("headq_workspace_status",
+               lib().headq_workspace_status(_ptr(ws), ctypes.c_void_p(s.cuda_stream)))

@@ -53,3 +53,33 @@ def test_sizes_past_32_bits_are_refused(hq, kw):
     if kw:
         with pytest.raises(ValueError, match="32 bits"):
             hq.tree_workspace(paged(hq), 4, kw.get("n", 1), kw.get("T"))
+
+
+def test_the_status_of_a_workspace_is_read_on_its_own_device(hq, monkeypatch):
+    """Whatever device is current: the stream waited for is the workspace's device's."""
+    seen = []
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            seen.append(("enter", self.device))
+
+        def __exit__(self, *a):
+            seen.append(("exit", self.device))
+
+    def status(ws, stream):
+        seen.append(("status", ws.value, stream.value))
+        return 0
+
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda d=None: types.SimpleNamespace(cuda_stream={None: 5}.get(d, 9)))
+    monkeypatch.setattr(hq, "lib", lambda: types.SimpleNamespace(headq_workspace_status=status))
+    ws = torch.zeros(256, dtype=torch.uint8)
+    hq.headq_workspace_status(ws)
+    assert seen == [("enter", ws.device), ("status", ws.data_ptr(), 9), ("exit", ws.device)]
+    del seen[:]
+    hq.headq_workspace_status(ws, stream=types.SimpleNamespace(cuda_stream=7))
+    assert seen[1] == ("status", ws.data_ptr(), 7)
