@@ -1,10 +1,11 @@
-"""The packed-batch operators where numbers leave the ordinary range."""
+"""The packed-batch operators where numbers leave the ordinary range, or pages the pool."""
 
 import numpy as np
 import pytest
 import torch
 
 from packed_helpers import Cache, check_tree, logical, ref_tree
+from test_gpu_packed import expected_planes, new_tokens
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -202,3 +203,35 @@ def test_a_lone_token_is_its_value(d, r):
     out = hq().headq_tree_attn(c.hq, q, c.U, T=1)
     v = hq().headq_cache_read(c.hq, c.U, n=1, T=1, dtype=F32)[1]
     assert torch.equal(out, v.repeat_interleave(2, 1))
+
+
+# ---------------------------------------------------------------- bad pages
+
+@pytest.mark.parametrize("Hq,d,r,n", [(4, 128, 16, 1), (14, 128, 16, 1), (4, 128, 16, 5), (4, 128, 16, 100),
+                                      (4, 32, 4, 3)])
+def test_a_bad_page_is_reported_and_touches_its_own_sequence_only(Hq, d, r, n):
+    c = Cache(120, 3, 2, 192, d, r, page=64)
+    good = [b for b in range(3) if b != 1]
+    lens = [192, 180, 150]
+    kk, vv = new_tokens(np.random.default_rng(2), 3 * n, 2, d, BF)
+    want = expected_planes(c, kk, vv, [n] * 3, lens)
+    table = c.table.clone()
+    for bad in (-1, 99999):
+        c.table.copy_(table)
+        c.table[1, 1 if n > 1 else 2] = bad
+        q = torch.randn(3 * n, Hq, d, generator=torch.Generator().manual_seed(n)).cuda().to(BF)
+        hq().headq_cache_write_ragged(c.hq, kk, vv, c.U, seq_lens=lens_of(lens), n=n)
+        for name, t in c.planes.items():
+            assert torch.equal(logical(t, table)[good].view(torch.uint8), want[name][good].view(torch.uint8)), name
+        ws = hq().tree_workspace(c.hq, Hq, n)
+        lse = torch.zeros(3 * n, Hq, device="cuda")
+        out = hq().headq_tree_attn(c.hq, q, c.U, seq_lens=lens_of(lens), n=n, ws=ws, lse=lse)
+        with pytest.raises(hq().HeadQError):
+            hq().headq_workspace_status(ws)
+        hq().headq_workspace_status(ws)
+        c.table.copy_(table)
+        ref = ref_tree(c, q, [n] * 3, lens, None)
+        rows = [b * n + i for b in good for i in range(n)]
+        check_tree(out[rows], lse[rows], [a[rows] for a in ref])
+        hq().headq_tree_attn(c.hq, q, c.U, seq_lens=lens_of(lens), n=n, ws=ws)
+        hq().headq_workspace_status(ws)                    # nothing left of it
