@@ -594,7 +594,7 @@ def _rows(t, name, heads, d, written=False):
     if len(shape) != 3 or shape[1] != heads or shape[2] != d:
         raise ValueError("%s must be [rows, %d, %d], got %s" % (name, heads, d, list(shape)))
     rows, code = shape[0], _dtype_code(t)
-    rs, hs, cs = t.stride()
+    rs, hs, cs = t.stride() if rows else (0, 0, 1)  # no rows: whatever the strides are
     per = 4 if code == HEADQ_F32 else 8
     if rows <= 1:  # the strides of a single row or head are never used
         rs = 0
@@ -603,7 +603,7 @@ def _rows(t, name, heads, d, written=False):
     if cs != 1 or rs % per or hs % per:
         raise ValueError("%s: channels must be contiguous and the other strides multiples of 16 bytes"
                          % name)
-    if written and not (rs >= heads * hs >= heads * d):  # not the plain order: what lies inside what
+    if written and rows and not (rs >= heads * hs >= heads * d):  # not the plain order: what lies inside what
         if rows > 1 and heads > 0:
             lo, hi = sorted(((rs, rows), (hs, heads))) if heads > 1 else ((d, 1), (rs, rows))
             if lo[0] < d or hi[0] < (lo[1] - 1) * lo[0] + d:

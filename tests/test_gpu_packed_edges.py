@@ -235,3 +235,23 @@ def test_a_bad_page_is_reported_and_touches_its_own_sequence_only(Hq, d, r, n):
         check_tree(out[rows], lse[rows], [a[rows] for a in ref])
         hq().headq_tree_attn(c.hq, q, c.U, seq_lens=lens_of(lens), n=n, ws=ws)
         hq().headq_workspace_status(ws)                    # nothing left of it
+
+
+# ---------------------------------------------------------------- nothing
+
+def test_batches_without_rows():
+    """No sequence takes part: every call returns, whatever strides the empty tensors have."""
+    c = Cache(140, 2, 2, 64, 64, 8)
+    before = {n: t.clone() for n, t in c.planes.items()}
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    empty = torch.from_numpy(np.empty((0, 2, 64), np.float32)).cuda().to(BF)
+    sliced = torch.empty(3, 64, 2, dtype=BF, device="cuda").transpose(1, 2)[:0]
+    for t in (empty, sliced):
+        hq().headq_cache_write_ragged(c.hq, t, t, c.U, cu=cu, n=3)
+        k, v = hq().headq_cache_read(c.hq, c.U, cu=cu, n=3, k_out=t, v_out=t)
+        out = hq().headq_tree_attn(c.hq, t, c.U, cu=cu, n=3, out=t)
+        assert k.shape == v.shape == out.shape == (0, 2, 64)
+    assert hq().headq_tree_attn(c.hq, empty, c.U).shape == (0, 2, 64)
+    assert hq().headq_cache_read(c.hq, c.U, n=0)[0].shape == (0, 2, 64)
+    for n, t in c.planes.items():
+        assert torch.equal(t, before[n]), n
