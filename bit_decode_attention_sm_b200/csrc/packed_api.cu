@@ -85,9 +85,10 @@ HEADQ_API headq_status headq_cache_write_ragged(const headq_cache* cache, const 
   if (st != HEADQ_OK) return st;
   if (cache->kmode != HEADQ_K_TOKEN) return HEADQ_ERR_UNSUPPORTED;  // sealed key blocks
   if ((st = check_span(span, cache)) != HEADQ_OK) return st;
-  if (src_rows < 0 || (src && !aligned16(src)) || (!src && src_rows != span->rows))
-    return HEADQ_ERR_INVALID_ARG;
+  if (src_rows < 0 || (src && !aligned16(src))) return HEADQ_ERR_INVALID_ARG;
   if (span->n == 0 || span->rows == 0 || cache->B == 0) return HEADQ_OK;
+  if (!src && src_rows != span->rows) return HEADQ_ERR_INVALID_ARG;
+  if (src_rows == 0) return HEADQ_OK;  // no token has a row to come from
   if ((st = check_rows(k)) != HEADQ_OK || (v && (st = check_rows(v)) != HEADQ_OK)) return st;
   if (v && v->dtype != k->dtype) return HEADQ_ERR_INVALID_ARG;
   if (cache->r > 0 && (!U || !aligned16(U))) return HEADQ_ERR_INVALID_ARG;

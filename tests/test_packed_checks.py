@@ -5,7 +5,8 @@ import types
 import pytest
 import torch
 
-from test_abi_host import hq  # noqa: F401  (the fixture)
+from test_abi_host import FAKE, hq  # noqa: F401  (hq: the fixture)
+from test_packed_host import rows, span, write
 
 
 def paged(hq, **kw):
@@ -83,3 +84,11 @@ def test_the_status_of_a_workspace_is_read_on_its_own_device(hq, monkeypatch):
     del seen[:]
     hq.headq_workspace_status(ws, stream=types.SimpleNamespace(cuda_stream=7))
     assert seen[1] == ("status", ws.data_ptr(), 7)
+
+
+def test_a_gathered_write_of_nothing(hq):
+    """No packed rows (an empty src has no address), or nothing to take them from."""
+    assert write(hq, sp=span(hq, n=4, rows=0, cu=FAKE), src=None, src_rows=7) == 0
+    assert write(hq, k=rows(hq, ptr=None), v=rows(hq, ptr=None), src=FAKE, src_rows=0) == 0
+    assert write(hq, src=None, src_rows=7) == 1
+    assert write(hq, src=FAKE + 4, sp=span(hq, n=4, rows=0, cu=FAKE)) == 1
