@@ -1088,6 +1088,9 @@ cudaError_t launch_dr(const TreeParams& p, const TreeMma& t, int grid_splits, bo
   const long long warps = static_cast<long long>(p.c.B) * p.c.Hkv * t.blocks * (kBlock / kPrepRows);
   const int row_ctas = static_cast<int>((warps + 7) / 8);
   const int mask_ctas = t.words ? (p.c.B * p.span.n + 7) / 8 : 0;
+  // Launched in plain stream order, not early like the two kernels behind it: once it starts, all
+  // work before this call is complete, so that the main kernel may read the cache and write empty
+  // partials without waiting.
   tree_prep_kernel<D, R><<<row_ctas + mask_ctas, 256, 0, s>>>(p, t, row_ctas);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;

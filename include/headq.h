@@ -474,7 +474,7 @@ headq_status headq_cache_read(const headq_cache *cache, const headq_span *span, 
  * truncated to bf16 (and summed as truncated), so out carries about 2 roundings to bf16; values below 2^-66 in size lose bits as
  * subnormal numbers do, and below 2^-89 count as 0.  Of those, calls with n = 1 and
  * Hq / Hkv <= 8 run the kernels of headq_decode_attn (but for 2-bit values with r = 0, and
- * for B * Hkv > 8192).  Every other shape, and fp32 q, is computed in fp32.  HEADQ_K_TOKEN
+ * for B * Hkv > 8192), which round the scales of 2-bit values, times the weights, to 11 bits.  Every other shape, and fp32 q, is computed in fp32.  HEADQ_K_TOKEN
  * caches only.
  */
 headq_status headq_tree_attn(const headq_cache *cache, const headq_rows *q, int Hq,
