@@ -757,6 +757,8 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       const int k = y >> 1, h = y & 1;
       if (k >= 0) {
         const int tile = tile_of(l, k), s = tile % VS;
+        // the stage's last tile was the other lane's: it is read before this one's phase counts
+        if (!V2 && !PAIR && h == 0 && tile >= VS && !wait(v_empty(s), tile / VS - 1)) break;
         // (the values first, while the weights are not there: a wait costs some 150 cycles anyway)
         if ((h == 0 && !wait(v_full(s), tile / VS)) || !wait(p_full(l, h), k)) break;
         tc_fence_after();
@@ -867,7 +869,10 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
           }
         }
       } else if (tail) {
-        // the last rows of the value tile: nothing past the end, and as above for new tokens
+        // the last rows of the value tile: nothing past the end, and as above for new tokens.
+        // A wait for one phase of a barrier passes while the phase before it is open, and this
+        // thread has not waited for the stage's earlier tiles: first until the last one is read.
+        if (k >= VS && ok && !mbar_wait(v_empty(sv), ((k / VS) - 1) & 1)) ok = false;
         if (ok && !mbar_wait(v_full(sv), (k / VS) & 1)) ok = false;
         uint8_t* vs = sm + Ly::kV + sv * Ly::kVTile;
         if (t0 + tok >= P) {
