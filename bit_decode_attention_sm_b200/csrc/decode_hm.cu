@@ -292,7 +292,13 @@ decode_hm_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap vmap)
   for (int j = warp; j < ntiles * kSlices; j += kCW) {
     const int i = j / kSlices, jw = 16 * (j - i * kSlices);
     const int s = i % kStages;
-    if (!mbar_wait(smem_addr(&bars[s]), (i / kStages) & 1)) {
+    // A wait for one phase of a barrier passes while the phase before it is open.  The warp has
+    // waited for the stage's last tile itself, unless it had no slice of that one: then first
+    // until it is consumed (which this tile's load waits for as well).
+    const int last = i - kStages;
+    if ((last >= 0 && (warp + (kCW - kSlices) * last) % kCW >= kSlices &&
+         !mbar_wait(smem_addr(&bars[kStages + s]), (last / kStages) & 1)) ||
+        !mbar_wait(smem_addr(&bars[s]), (i / kStages) & 1)) {
       ok = false;
       break;
     }

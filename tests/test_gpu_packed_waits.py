@@ -40,3 +40,23 @@ def test_late_values(i, copies):
     check_tree(outs[0], None, ref)
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,r,vmode", [(28, 4, 128, 16, "dense"), (14, 2, 64, 8, "2bit"), (8, 2, 128, 0, "dense")])
+def test_late_tiles_of_single_tokens(Hq, Hkv, d, r, vmode):
+    """The decode kernels' warps, not all of which have a part in every tile."""
+    from bit_decode_attention_sm_b200 import headq
+    B, T = 24, 2048
+    c = Cache(230, B, Hkv, T, d, r, vmode, BF, 64)
+    rng = np.random.default_rng(1)
+    q = torch.from_numpy(rng.standard_normal((B, Hq, d)).astype(np.float32) * 1.5).cuda().to(BF)
+    lens = [int(x) for x in rng.integers(T // 2, T + 1, B)]
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    outs = []
+    for k in range(40):
+        flush.fill_(k)
+        outs.append(headq.headq_tree_attn(c.hq, q, c.U, seq_lens=sl))
+    check_tree(outs[0], None, ref_tree(c, q, [1] * B, lens, None))
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
