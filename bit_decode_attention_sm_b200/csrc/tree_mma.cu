@@ -5,7 +5,11 @@
 // The n * G query rows of a (sequence, KV head) fill the M side of tcgen05.mma, 128 rows a
 // block; 128-token tiles of the cache are the N side of the logits and the K side of the
 // readout.  A logit is one dot product of length d + r: q with the decoded base key, and
-// U_h^T q with the decoded side code.
+// U_h^T q with the decoded side code.  Both sides of the latter are fp16 in two parts (22 bits;
+// the product of the two smaller parts is left out): in one part each they were the largest
+// errors behind the output's own rounding (against 64 bits 0.0025 on the long context, now
+// 0.0018, of which the output's is 0.0016), for two more K steps of eleven, 188 -> 196 us there
+// and 0 to 2 % elsewhere.
 //
 // tree_prep_kernel   once per call: query rows as fp16 operands, each scaled by its own
 //   power of two (exact for bf16 queries but for elements 2^-28 below the row's largest),
@@ -26,9 +30,9 @@
 // The running maximum is kept with a slack of 2^60 (kSlack): one pass over the logits and no
 // search for the maximum in it, and the output accumulator in TMEM is rescaled only when a
 // weight reaches 2, which is rare (with a slack of 2^8 it was a third of the steps in peaked
-// attention).  Weights are truncated to bf16 and the sum is taken over the truncated weights,
-// so that the error of a weight cancels where one token holds most of it; the log-sum-exp,
-// when asked for, is summed over the unrounded ones.
+// attention).  Weights are rounded to bf16 and the sum is taken over the rounded weights, so that
+// the error of a weight cancels where one token holds most of it; the log-sum-exp, when asked
+// for, is summed over the unrounded ones.
 //
 // Measured: 64 new tokens over 131072 cached ones, 32 heads on 8, 171 us (its products take 89
 // at the rate of a large matrix product); 32 over 64 x 4096 in 2-bit values, 28 heads on 4,
@@ -63,7 +67,7 @@ constexpr int kThreads = 20 * 32;  // five whole warpgroups
 constexpr int kRegsSoftmax = 128, kRegsDecode = 80, kRegsOther = 48;
 constexpr int kDecodeWarp = 8, kMmaWarp = 16, kTmaWarp = 18;  // one MMA warp per lane
 constexpr int kKStages = 2;
-constexpr int kRing = 8;            // tiles whose key scales are kept (more than can be in flight)
+constexpr int kRing = 8;            // tiles whose key scales are kept (more than can be in flight), a byte each
 // A row's weights are 2^(logit - m) with m at least the largest logit so far and, when it is
 // set, kSlack above it: the check that a step stays below 2 is then one bit of the weights,
 // and m is seldom set again.  Weights and sums have the 8-bit exponent of fp32, so the offset
@@ -76,8 +80,10 @@ constexpr float kSlack = 60.0f;
 constexpr uint32_t kAll = 0xffffffffu;
 
 // bytes of 128 operand rows: d channels in 64-channel blocks (128-byte rows, 128-byte
-// swizzle), then 16 side entries (two 8-entry halves, no swizzle)
-__host__ __device__ constexpr int operand_bytes(int d, int r) { return kTile * (2 * d + (r > 0 ? 32 : 0)); }
+// swizzle), then 16 side entries (two 8-entry halves, no swizzle), then what their rounding to
+// fp16 left, laid out the same
+constexpr int kSideBytes = kTile * 32;
+__host__ __device__ constexpr int operand_bytes(int d, int r) { return kTile * 2 * d + (r > 0 ? 2 * kSideBytes : 0); }
 
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -373,8 +379,16 @@ tree_prep_kernel(const TreeParams p, const TreeMma t, int row_ctas) {
     if constexpr (R > 0) {
       __half* zb = reinterpret_cast<__half*>(img + D / 64 * (kTile * 128));
       const int e = ll / (LPR / R);
-      if (ll % (LPR / R) == 0) zb[(e / 8) * (kTile * 8) + xr * 8 + (e & 7)] = __float2half_rn(side * s.x);
-      if (R == 8 && ll < 8) zb[kTile * 8 + xr * 8 + ll] = __float2half_rn(0.0f);
+      if (ll % (LPR / R) == 0) {
+        const __half hi = __float2half_rn(side * s.x);
+        __half* at = zb + (e / 8) * (kTile * 8) + xr * 8 + (e & 7);
+        at[0] = hi;
+        at[kSideBytes / 2] = __float2half_rn(side * s.x - __half2float(hi));
+      }
+      if (R == 8 && ll < 8) {
+        __half* at = zb + kTile * 8 + xr * 8 + ll;
+        at[0] = at[kSideBytes / 2] = __float2half_rn(0.0f);
+      }
     }
     if (ll == 0)
       t.qf[static_cast<size_t>(unit) * t.blocks * kBlock + x] = s.y * (fabsf(p.sm_scale) * dc::kLog2e);
@@ -390,8 +404,8 @@ struct Layout {
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + (PAIR ? 2 : 1) * kOperand;
   static constexpr int kV = kK + kKStages * kOperand;
-  static constexpr int kScale = kV + kVStages * kVTile;  // [kRing][kTile] floats
-  static constexpr int kBars = kScale + kRing * kTile * 4;
+  static constexpr int kScale = kV + kVStages * kVTile;  // [kRing][kTile] bytes: exponents of powers of two
+  static constexpr int kBars = kScale + kRing * kTile;
   static constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 12;
   static constexpr int kMisc = (kBars + 8 * kNumBars + 15) & ~15;  // tmem base, bad-value flag, 2 x 8 maxima
   static constexpr int kBytes = kMisc + 128 + 1024;    // and room for the alignment
@@ -491,7 +505,7 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int wpr, int 
   return __funnelshift_r(mask_word(row, wpr, i, k), mask_word(row, wpr, i, k + 1), a & 31);
 }
 
-// Running maximum (log2 units), sum of the truncated weights, sum of the exact ones.
+// Running maximum (log2 units), sum of the rounded weights, sum of the exact ones.
 struct RowState {
   float m, l, lx;
 };
@@ -521,20 +535,26 @@ __device__ __forceinline__ RowState raise_max(RowState st, float top, uint32_t t
 
 constexpr int kHalf = kTile / 2;
 
+// a power of two from its exponent field
+__device__ __forceinline__ float pow2_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
 // The logits of half a tile that holds new tokens or ends the sequence, in TMEM: each token
 // has its own scale, and is masked.  a: new-token index of the half's first token; f: the row's
 // factor to log2 units.
-__device__ __forceinline__ void mask_half(uint32_t ts, const uint32_t* row, int wpr, int i, int a, const float* col,
-                                          float f) {
+__device__ __forceinline__ void mask_half(uint32_t ts, const uint32_t* row, int wpr, int i, int a,
+                                          const uint8_t* col, float f) {
 #pragma unroll 1
   for (int c = 0; c < kHalf; c += 16) {
     uint32_t w[16];
     tc_ld16(ts + c, w);
     const uint32_t bits = mask_bits(row, wpr, i, a + c);
+    const uint4 e4 = *reinterpret_cast<const uint4*>(col + c);
+    const uint32_t e[4] = {e4.x, e4.y, e4.z, e4.w};
     tc_wait_ld();
 #pragma unroll
     for (int j = 0; j < 16; ++j)
-      w[j] = __float_as_uint((bits >> j) & 1u ? __uint_as_float(w[j]) * col[c + j] * f : -INFINITY);
+      w[j] = __float_as_uint((bits >> j) & 1u ? __uint_as_float(w[j]) * pow2_of((e[j / 4] >> (8 * (j % 4))) & 255u) * f
+                                               : -INFINITY);
     tc_st16(ts + c, w, 0);
   }
   tc_wait_st();
@@ -552,11 +572,9 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[kHalf], float f, flo
 #pragma unroll
   for (int j = 0; j < kHalf / 2; ++j) {
     const uint64_t y = codec::fma2(codec::pk2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), f2, m2);
-    const uint32_t h0 = __float_as_uint(ex2(codec::pk_lo(y))) & 0xffff0000u;
-    const uint32_t h1 = __float_as_uint(ex2(codec::pk_hi(y))) & 0xffff0000u;
-    w[j] = __byte_perm(h0, h1, 0x7632);
+    w[j] = pack_bf16(ex2(codec::pk_lo(y)), ex2(codec::pk_hi(y)));
     any[j & 1] |= w[j];
-    a[j & 1] = codec::add2(a[j & 1], codec::pk2(__uint_as_float(h0), __uint_as_float(h1)));
+    a[j & 1] = codec::add2(a[j & 1], codec::pk2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u)));
   }
   const uint64_t t = codec::add2(a[0], a[1]);
   sum = codec::pk_lo(t) + codec::pk_hi(t);
@@ -633,7 +651,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
 
   uint8_t* sm = smem_align(raw_smem, 1024);
   const uint32_t base = smem_addr(sm);
-  float* scale_s = reinterpret_cast<float*>(sm + Ly::kScale);
+  uint8_t* scale_s = sm + Ly::kScale;
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + Ly::kMisc);
   const uint32_t bars = base + Ly::kBars;
   const uint32_t q_full = bars;
@@ -779,8 +797,12 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
           const uint32_t off = ((e >> 2) * (kTile * 128) + 32 * (e & 3)) >> 4;
           tc_mma_ss(d, q_lo + off, kSwz, k_lo + ka + off, kSwz, kLogit, e > 0, one);
         }
-        if constexpr (R > 0)
-          tc_mma_ss(d, qs_lo, kFlat, ks_lo + ((s * Ly::kOperand + 1024 * h) >> 4), kFlat, kLogit, true, one);
+        if constexpr (R > 0) {  // both sides' leading parts, then each with what the other's rounding left
+          const uint32_t ks = ks_lo + ((s * Ly::kOperand + 1024 * h) >> 4);
+          tc_mma_ss(d, qs_lo, kFlat, ks, kFlat, kLogit, true, one);
+          tc_mma_ss(d, qs_lo + (kSideBytes >> 4), kFlat, ks, kFlat, kLogit, true, one);
+          tc_mma_ss(d, qs_lo, kFlat, ks + (kSideBytes >> 4), kFlat, kLogit, true, one);
+        }
         tc_commit(s_full(l, h), one);
         if (h == 1) tc_commit(k_empty(s), one);
       }
@@ -819,7 +841,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         mx = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
       }
       const float2 sc = operand_scale(mx);
-      if (half == 0) scale_s[(k % kRing) * kTile + tok] = sc.y;
+      if (half == 0) scale_s[(k % kRing) * kTile + tok] = static_cast<uint8_t>(__float_as_uint(sc.y) >> 23);
       uint8_t* ks = sm + Ly::kK + s * Ly::kOperand;
 #pragma unroll
       for (int g = 0; g < HG; ++g) {
@@ -836,7 +858,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
       }
       if constexpr (R > 0) {
         const float zs = cur.zs * sc.x;
-        uint32_t o[4] = {0, 0, 0, 0};
+        uint32_t o[4] = {0, 0, 0, 0}, left[4] = {0, 0, 0, 0};
         if (8 * half < R) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -845,9 +867,13 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
             const float a = __uint_as_float((w & 15u) ^ 0x4B000008u) - 8388616.0f;
             const float c = __uint_as_float(((w >> 4) & 15u) ^ 0x4B000008u) - 8388616.0f;
             o[e] = pack_f16(a * zs, c * zs);
+            const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&o[e]));
+            if (fabsf(zs) < INFINITY) left[e] = pack_f16(fmaf(a, zs, -r.x), fmaf(c, zs, -r.y));
           }
         }
-        reinterpret_cast<uint4*>(ks + D / 64 * (kTile * 128))[half * kTile + tok] = make_uint4(o[0], o[1], o[2], o[3]);
+        uint4* side = reinterpret_cast<uint4*>(ks + D / 64 * (kTile * 128)) + half * kTile + tok;
+        side[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        side[kSideBytes / 16] = make_uint4(left[0], left[1], left[2], left[3]);
       }
       if constexpr (V2) {
         if (k >= VS && ok && !mbar_wait(v_empty(sv), ((k / VS) - 1) & 1)) ok = false;
@@ -967,10 +993,10 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
           ok = __all_sync(kAll, ok && mbar_wait(bar, parity));
         }
         const int tile = tile_of(wl, (y + 1) >> 1);
-        const float* col = scale_s + (tile % kRing) * kTile;
+        const uint8_t* col = scale_s + (tile % kRing) * kTile;
         const uint32_t sa = ts + kHalf * (1 - h);
         tc_fence_after();
-        f = fmaxf(fq * col[0], 1e-37f);
+        f = fmaxf(fq * pow2_of(col[0]), 1e-37f);
         if (tile >= round_from) {
           mask_half(sa, words, t.wpr, i, t_lo + tile * kTile + kHalf * (1 - h) - P, col + kHalf * (1 - h),
                     fmaxf(fq, 1e-37f));
@@ -1006,7 +1032,7 @@ tree_mma_kernel(const TreeParams p, const TreeMma t, const __grid_constant__ CUt
         }
         tc_wait_st();
       }
-// 32 columns at a time.  PAIR: through shared memory (the lane's query image, which its
+      // 32 columns at a time.  PAIR: through shared memory (the lane's query image, which its
       // products no longer read), so that 8 lanes store one row's 128 bytes where each lane
       // storing its own row touches 32 lines an instruction (9000 cycles a CTA).
       float4* turn = reinterpret_cast<float4*>(sm + Ly::kQ + (PAIR ? wl : 0) * Ly::kOperand) + (warp & 3) * 256;

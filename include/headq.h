@@ -470,12 +470,14 @@ headq_status headq_cache_read(const headq_cache *cache, const headq_span *span, 
  *         n new tokens a sequence and span->T up to T; zero-filled before first use; its
  *         first word is the device error word.  Calls sharing it must not overlap on the GPU.
  * bf16 q with bf16 or 2-bit values, d 64 or 128 and r 0, 8 or 16 runs on the tensor cores:
- * keys are rounded to 11 bits relative to the largest of their tile and softmax weights
- * truncated to bf16 (and summed as truncated), so out carries about 2 roundings to bf16; values below 2^-66 in size lose bits as
- * subnormal numbers do, and below 2^-89 count as 0.  Of those, calls with n = 1 and
- * Hq / Hkv <= 8 run the kernels of headq_decode_attn (but for 2-bit values with r = 0, and
- * for B * Hkv > 8192), which round the scales of 2-bit values, times the weights, to 11 bits.  Every other shape, and fp32 q, is computed in fp32.  HEADQ_K_TOKEN
- * caches only.
+ * base keys are rounded to 11 bits relative to the largest of their tile, softmax weights and
+ * 2-bit values to bf16 (weights are summed as rounded).  At logits of a standard deviation of
+ * 12 the errors of these together are half (2-bit values: three quarters) of the rounding of
+ * out.  Values below 2^-66 in size lose bits as subnormal numbers do, and below 2^-89 count
+ * as 0.  Of those calls, the ones with n = 1 and Hq / Hkv <= 8 run the kernels of
+ * headq_decode_attn (but for 2-bit values with r = 0, and for B * Hkv > 8192), which round
+ * the scales of 2-bit values, times the weights, to 11 bits.  Every other shape, and fp32 q,
+ * is computed in fp32.  HEADQ_K_TOKEN caches only.
  */
 headq_status headq_tree_attn(const headq_cache *cache, const headq_rows *q, int Hq,
                              const uint8_t *mask, long long mask_stride, const headq_span *span,
