@@ -621,12 +621,10 @@ def _int32(t, name, shape):
     return t.data_ptr()
 
 
-def _int(x, name):
-    """x as the C structures hold it; ctypes would wrap a larger one."""
-    x = int(x)
-    if not -0x80000000 <= x <= 0x7fffffff:
-        raise ValueError("%s = %d does not fit 32 bits" % (name, x))
-    return x
+def _fits(T, n, rows=0):
+    """The sizes fit the C structures; ctypes would wrap larger ones."""
+    if not (-0x80000000 <= T <= 0x7fffffff and -0x80000000 <= n <= 0x7fffffff and rows <= 0x7fffffff):
+        raise ValueError("T = %d, n = %d, %d rows: more than 32 bits" % (T, n, rows))
 
 
 def _span(cache, seq_lens, cu, n, T, rows):
@@ -637,8 +635,9 @@ def _span(cache, seq_lens, cu, n, T, rows):
         if cache.B and rows % cache.B:
             raise ValueError("%d rows are no whole number for each of %d sequences" % (rows, cache.B))
         n = rows // cache.B if cache.B else 0
-    return SpanStruct(_int32(seq_lens, "seq_lens", (cache.B,)), _int32(cu, "cu", (cache.B + 1,)),
-                      cache.T_cap if T is None else _int(T, "T"), _int(n, "n"), _int(rows, "rows"))
+    n, T = int(n), cache.T_cap if T is None else int(T)
+    _fits(T, n, rows)
+    return SpanStruct(_int32(seq_lens, "seq_lens", (cache.B,)), _int32(cu, "cu", (cache.B + 1,)), T, n, rows)
 
 
 def _basis(cache, U):
@@ -700,7 +699,8 @@ def tree_workspace(cache, Hq, n, T=None, stream=None):
     """A zeroed device workspace for headq_tree_attn with up to n new tokens per sequence and
     lengths up to T (None: the capacity)."""
     cs = cache.struct()
-    n, T = _int(n, "n"), cache.T_cap if T is None else _int(T, "T")
+    n, T = int(n), cache.T_cap if T is None else int(T)
+    _fits(T, n)
     with torch.cuda.device(cache.k_codes.device):
         nb = lib().headq_tree_workspace_bytes(cs, Hq, n, T)
     return _zeros(max(nb, 256), torch.uint8, cache.k_codes.device, stream)
