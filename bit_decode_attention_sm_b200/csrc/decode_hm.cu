@@ -288,16 +288,19 @@ decode_hm_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap vmap)
   bool ok = true;
   // The kCW warps take the kSlices 16-token slices of the stages in turn (slice
   // j = tile j / kSlices, tokens 16 (j % kSlices) ..), each with its own online
-  // softmax; a stage is released after its kSlices slices.
+  // softmax; a stage is released after its kSlices slices.  With one slice a tile
+  // fewer than warps, a warp passes over every kCW-th tile (passed: the last one).
+  static_assert(kSlices == kCW - 1, "tiles passed over");
+  int passed = kCW - 1 - warp - kCW;
   for (int j = warp; j < ntiles * kSlices; j += kCW) {
     const int i = j / kSlices, jw = 16 * (j - i * kSlices);
     const int s = i % kStages;
     // A wait for one phase of a barrier passes while the phase before it is open.  The warp has
-    // waited for the stage's last tile itself, unless it had no slice of that one: then first
-    // until it is consumed (which this tile's load waits for as well).
-    const int last = i - kStages;
-    if ((last >= 0 && (warp + (kCW - kSlices) * last) % kCW >= kSlices &&
-         !mbar_wait(smem_addr(&bars[kStages + s]), (last / kStages) & 1)) ||
+    // waited for the stage's last tile itself, unless it passed over that one: then first until
+    // it is consumed (which this tile's load waits for as well).
+    if (i > passed + kCW) passed += kCW;
+    if ((i - passed == kStages % kCW && i >= kStages &&
+         !mbar_wait(smem_addr(&bars[kStages + s]), ((i / kStages) - 1) & 1)) ||
         !mbar_wait(smem_addr(&bars[s]), (i / kStages) & 1)) {
       ok = false;
       break;
