@@ -30,17 +30,17 @@
 // The running maximum is kept with a slack of 2^60 (kSlack): one pass over the logits and no
 // search for the maximum in it, and the output accumulator in TMEM is rescaled only when a
 // weight reaches 2, which is rare (with a slack of 2^8 it was a third of the steps in peaked
-// attention; kSlack has what the offset costs).  Weights are rounded to bf16 and the sum is taken over the rounded weights, so that
-// the error of a weight cancels where one token holds most of it; the log-sum-exp, when asked
-// for, is summed over the unrounded ones.
+// attention; kSlack has what the offset costs).  Weights are rounded to bf16 and the sum is taken
+// over the rounded weights, so that the error of a weight cancels where one token holds most of
+// it; the log-sum-exp, when asked for, is summed over the unrounded ones.
 //
 // Measured: 64 new tokens over 131072 cached ones, 32 heads on 8, 177 us (its products take 89
 // at the rate of a large matrix product); 32 over 64 x 4096 in 2-bit values, 28 heads on 4,
 // 227 us (78).  The exponential units are 45 % busy, the tensor pipe 52 %, the issue slots
 // 54 %; what bounds the kernel is that a tile passes five hand-overs (decoder, logits, weights,
-// readout, release), each some 150 cycles even when nothing is left to wait for.  Measured
-// while the long case stood at 180: sixteen softmax warps 193, lanes in ping-pong 231, one row block per CTA
-// with three logit buffers 201.  A CTA's set-up, first tile and outputs are some 8 us; the
+// readout, release), each some 150 cycles even when nothing is left to wait for.  Measured while
+// the long case stood at 180: sixteen softmax warps 193, lanes in ping-pong 231, one row block per
+// CTA with three logit buffers 201.  A CTA's set-up, first tile and outputs are some 8 us; the
 // kernel therefore starts on the cache while the queries are still being prepared.
 //
 // TMEM (512 columns): logits of lane l at 128 l (its weights overwrite them, two to a
